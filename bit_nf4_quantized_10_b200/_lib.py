@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_HERE, "libqlora_nf4.so")
 QL_OK, QL_ERR_INVALID_ARG, QL_ERR_UNSUPPORTED, QL_ERR_WORKSPACE, QL_ERR_CUDA, QL_ERR_NONFINITE, QL_ERR_TIMEOUT = range(7)
 QL_F32, QL_BF16 = 0, 1
 QL_OP_DOUBLE_QUANT, QL_OP_FWD, QL_OP_BWD, QL_OP_NVFP4 = 0, 1, 2, 3
+QL_OP_BLOCK_NORM_BWD, QL_OP_GRAD_NORM, QL_OP_INT8_GEMM = 4, 5, 6
 QL_PAGE_DEVICE, QL_PAGE_HOST = 0, 1
 
 EXPORTS = ("nf4_quantize", "nf4_double_quant", "nf4_double_quant_noalloc", "nf4_dequant", "qlora_linear_fwd", "qlora_linear_bwd",
@@ -26,7 +27,9 @@ EXPORTS = ("nf4_quantize", "nf4_double_quant", "nf4_double_quant_noalloc", "nf4_
            "nf4_codebook", "qlora_get_status", "qlora_status_string", "qlora_selftest_wait_timeout",
            "qlora_merge", "nf4_double_quant_level1", "nf4_double_quant_finish", "nvfp4_quantize", "mxfp4_quantize",
            "nvfp4_dequant", "mxfp4_dequant", "qlora_adamw_step", "qlora_paged_prefetch", "nvfp4_scale_atoms_bytes",
-           "nvfp4_scale_atoms", "nvfp4_gemm", "mxfp4_scale_atoms_bytes", "mxfp4_scale_atoms", "mxfp4_gemm")
+           "nvfp4_scale_atoms", "nvfp4_gemm", "mxfp4_scale_atoms_bytes", "mxfp4_scale_atoms", "mxfp4_gemm",
+           "qlora_grad_norm", "qlora_grad_scale", "qlora_adamw_step_clipped", "qlora_block_norm_fwd",
+           "qlora_block_norm_bwd", "int8_quantize", "int8_gemm")
 
 
 class QLoraError(RuntimeError):
@@ -41,12 +44,24 @@ class ql_nf4_weight(ctypes.Structure):
                 ("cols", ctypes.c_int64)]
 
 
+class ql_tensor_list(ctypes.Structure):
+    _fields_ = [("data", ctypes.POINTER(ctypes.c_void_p)), ("numel", ctypes.POINTER(ctypes.c_int64)),
+                ("dt", ctypes.POINTER(ctypes.c_int32)), ("count", ctypes.c_int64)]
+
+
+class ql_block_norm(ctypes.Structure):
+    _fields_ = [("w_pre", ctypes.c_void_p), ("w_post", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("w_dt", ctypes.c_int), ("w_offset", ctypes.c_float), ("alpha", ctypes.c_float),
+                ("eps", ctypes.c_float), ("gate_rows", ctypes.c_int64)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing; build it with `python bit_nf4_quantized_10_b200/build.py`")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i64, i32, f32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
     W = ctypes.POINTER(ql_nf4_weight)
+    T, B = ctypes.POINTER(ql_tensor_list), ctypes.POINTER(ql_block_norm)
     sig = {
         "nf4_quantize": (i32, [vp, i32, i64, vp, vp, vp]),
         "nf4_double_quant": (i32, [vp, i64, vp, vp, vp, vp, sz, vp]),
@@ -77,6 +92,14 @@ def _load() -> ctypes.CDLL:
         "mxfp4_scale_atoms_bytes": (sz, [i64, i64]),
         "mxfp4_scale_atoms": (i32, [vp, i64, i64, vp, vp]),
         "mxfp4_gemm": (i32, [vp, vp, vp, vp, i64, i64, i64, vp, vp]),
+        "qlora_grad_norm": (i32, [T, f32, vp, vp, vp, sz, vp]),
+        "qlora_grad_scale": (i32, [T, vp, vp]),
+        "qlora_adamw_step_clipped": (i32, [vp, vp, vp, vp, vp, i64, i64, f32, f32, f32, f32, f32, vp, vp]),
+        "qlora_block_norm_fwd": (i32, [B, vp, i32, vp, i32, i64, i64, vp, vp, i32, vp, vp, vp]),
+        "qlora_block_norm_bwd": (i32, [B, vp, i32, vp, i32, vp, vp, vp, vp, i32, i64, i64, vp, vp, vp, vp, vp, vp, sz,
+                                       vp]),
+        "int8_quantize": (i32, [vp, i32, i64, i64, vp, vp, vp]),
+        "int8_gemm": (i32, [vp, vp, vp, vp, i64, i64, i64, vp, i32, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -279,6 +302,161 @@ def qlora_silu_gate_fwd(g, u, h, stream=None) -> None:
 def qlora_silu_gate_bwd(dh, g, u, dg, du, stream=None) -> None:
     _check(LIB.qlora_silu_gate_bwd(_ptr(dh), _ptr(g), _ptr(u), _ptr(dg), _ptr(du), g.numel(), _stream(stream)),
            "qlora_silu_gate_bwd")
+
+
+# The calls below take their sizes from the tensors, so they check that every
+# tensor is contiguous, of a known type, on the current device and as large as
+# the others make it: the library sees pointers only.
+def _buf(t, name: str, shape, dtypes=None) -> int | None:
+    """The address of a tensor of this shape, or None for None."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} instead of {tuple(shape)}")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
+    return t.data_ptr()
+
+
+_F32 = (torch.float32,)
+_F32_BF16 = (torch.float32, torch.bfloat16)
+_I8 = (torch.int8,)
+
+
+def _ws(ws) -> tuple[int | None, int]:
+    if ws is None:
+        return None, 0
+    return _buf(ws, "ws", ws.shape), ws.numel() * ws.element_size()
+
+
+class TensorList:
+    """The tensors of one gradient norm: fp32 or bf16, contiguous, 16-byte aligned,
+    on one device (see ql_tensor_list).  Holds the tensors and their description,
+    so that a list is described once and used every step."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        n = len(self.tensors)
+        self.device = self.tensors[0].get_device() if n else None
+        for i, t in enumerate(self.tensors):
+            if not t.is_cuda or t.get_device() != self.device:
+                raise ValueError(f"tensor {i}: on {t.device}; a list holds tensors of one CUDA device")
+            if not t.is_contiguous():
+                raise ValueError(f"tensor {i}: not contiguous")
+        self._data = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.tensors])
+        self._numel = (ctypes.c_int64 * n)(*[t.numel() for t in self.tensors])
+        self._dt = (ctypes.c_int32 * n)(*[_dt(t.dtype) for t in self.tensors])
+        self._desc = ql_tensor_list(ctypes.cast(self._data, ctypes.POINTER(ctypes.c_void_p)),
+                                    ctypes.cast(self._numel, ctypes.POINTER(ctypes.c_int64)),
+                                    ctypes.cast(self._dt, ctypes.POINTER(ctypes.c_int32)), n)
+
+    def __len__(self) -> int:
+        return len(self.tensors)
+
+    def desc(self) -> ql_tensor_list:
+        if self.device is not None and self.device != torch.cuda.current_device():
+            raise ValueError(f"the list is on cuda:{self.device}, not on the current CUDA device")
+        return self._desc
+
+
+def qlora_grad_norm(tensors: TensorList, max_norm: float, norm, coef, ws, stream=None) -> None:
+    """norm = sqrt(sum of squares over all tensors), coef = min(1, max_norm / (norm + 1e-6)); fp32 [1] outputs or None."""
+    wp, wb = _ws(ws)
+    _check(LIB.qlora_grad_norm(ctypes.byref(tensors.desc()), float(max_norm), _buf(norm, "norm", (1,), _F32),
+                               _buf(coef, "coef", (1,), _F32), wp, wb, _stream(stream)), "qlora_grad_norm")
+
+
+def qlora_grad_scale(tensors: TensorList, coef, stream=None) -> None:
+    """Every value of every tensor times coef [1] (a device value), in place."""
+    _check(LIB.qlora_grad_scale(ctypes.byref(tensors.desc()), _buf(coef, "coef", (1,), _F32), _stream(stream)),
+           "qlora_grad_scale")
+
+
+def qlora_adamw_step_clipped(p, g, m, v, n: int, t: int, lr: float, coef, beta1: float = 0.9, beta2: float = 0.999,
+                             eps: float = 1e-8, weight_decay: float = 0.0, p_bf16=None, stream=None) -> None:
+    """qlora_adamw_step on g times coef [1] (a device value, from qlora_grad_norm); g is only read."""
+    _check(LIB.qlora_adamw_step_clipped(_ptr(p), _ptr(g), _ptr(m), _ptr(v), _ptr(p_bf16), int(n), int(t), float(lr),
+                                        float(beta1), float(beta2), float(eps), float(weight_decay),
+                                        _buf(coef, "coef", (1,), _F32), _stream(stream)), "qlora_adamw_step_clipped")
+
+
+class BlockNorm:
+    """Weights and constants of the norms around one block (see ql_block_norm):
+    w_pre, w_post [D] and gate [G, D], all of one type, fp32 or bf16."""
+
+    def __init__(self, w_pre=None, w_post=None, gate=None, gate_rows: int = 0, alpha: float = 1.0, eps: float = 1e-6,
+                 w_offset: float = 0.0):
+        self.w_pre, self.w_post, self.gate = w_pre, w_post, gate
+        self.gate_rows, self.alpha, self.eps, self.w_offset = int(gate_rows), float(alpha), float(eps), float(w_offset)
+        given = [t for t in (w_pre, w_post, gate) if t is not None]
+        if any(t.dtype != given[0].dtype for t in given):
+            raise TypeError("w_pre, w_post and gate must have one dtype")
+        if gate is not None and (gate.dim() != 2 or self.gate_rows < 1):
+            raise ValueError("gate must be [gates, D] with gate_rows >= 1")
+        self._w_dt = _dt(given[0].dtype) if given else QL_F32
+        self._checked = None
+
+    def desc(self, M: int, D: int) -> ql_block_norm:
+        key = (M, D, torch.cuda.current_device())
+        if self._checked is None or self._checked[0] != key:
+            G = -(-M // self.gate_rows) if self.gate is not None else 0
+            self._checked = (key, ql_block_norm(_buf(self.w_pre, "w_pre", (D,)), _buf(self.w_post, "w_post", (D,)),
+                                                _buf(self.gate, "gate", (G, D)), self._w_dt, self.w_offset,
+                                                self.alpha, self.eps, self.gate_rows))
+        return self._checked[1]
+
+
+def qlora_block_norm_fwd(norm: BlockNorm, x, h, x_out, y, rstd_pre=None, rstd_post=None, stream=None) -> None:
+    """x_out = alpha x + gate * post_norm(h), y = pre_norm(x_out); h, x_out or y, and the saved rstd [M], may be None."""
+    M, D = shape = x.shape
+    d = norm.desc(M, D)
+    _check(LIB.qlora_block_norm_fwd(
+        ctypes.byref(d), _buf(x, "x", shape), _dt(x.dtype), _buf(h, "h", shape), 0 if h is None else _dt(h.dtype), M, D,
+        _buf(x_out, "x_out", shape, (x.dtype,)), _buf(y, "y", shape), 0 if y is None else _dt(y.dtype),
+        _buf(rstd_pre, "rstd_pre", (M,), _F32), _buf(rstd_post, "rstd_post", (M,), _F32), _stream(stream)),
+        "qlora_block_norm_fwd")
+
+
+def qlora_block_norm_bwd(norm: BlockNorm, x_out, h, rstd_pre, rstd_post, dx_out, dy, dx, dh, dw_pre=None, dw_post=None,
+                         dgate=None, ws=None, stream=None) -> None:
+    """Gradients of qlora_block_norm_fwd: dx [M, D] and dh [M, D] from dx_out and dy (either may be None), and the
+    fp32 sums dw_pre [D], dw_post [D] and dgate [G, D] where given (they need the workspace)."""
+    given = dy if dy is not None else dx_out
+    M, D = shape = given.shape
+    d = norm.desc(M, D)
+    stream_t = next((t for t in (x_out, dx_out, dx) if t is not None), None)
+    xt = stream_t.dtype if stream_t is not None else torch.float32
+    block_t = h if h is not None else dh
+    ht = block_t.dtype if block_t is not None else xt
+    G = d.gate_rows and -(-M // d.gate_rows)
+    wp, wb = _ws(ws)
+    _check(LIB.qlora_block_norm_bwd(
+        ctypes.byref(d), _buf(x_out, "x_out", shape, (xt,)), _dt(xt), _buf(h, "h", shape, (ht,)), _dt(ht),
+        _buf(rstd_pre, "rstd_pre", (M,), _F32), _buf(rstd_post, "rstd_post", (M,), _F32),
+        _buf(dx_out, "dx_out", shape, (xt,)), _buf(dy, "dy", shape), 0 if dy is None else _dt(dy.dtype), M, D,
+        _buf(dx, "dx", shape, (xt,)), _buf(dh, "dh", shape, (ht,)), _buf(dw_pre, "dw_pre", (D,), _F32),
+        _buf(dw_post, "dw_post", (D,), _F32), _buf(dgate, "dgate", (G, D), _F32), wp, wb, _stream(stream)),
+        "qlora_block_norm_bwd")
+
+
+def int8_quantize(x, codes, scales, stream=None) -> None:
+    """Rows of x [rows, K] to int8 codes [rows, K] and fp32 scales [rows]."""
+    rows, K = x.shape
+    _check(LIB.int8_quantize(_buf(x, "x", x.shape), _dt(x.dtype), rows, K, _buf(codes, "codes", x.shape, _I8),
+                             _buf(scales, "scales", (rows,), _F32), _stream(stream)), "int8_quantize")
+
+
+def int8_gemm(a_codes, a_scales, b_codes, b_scales, Y, ws=None, stream=None) -> None:
+    """Y [M, N] = (a_codes [M, K] b_codes [N, K]^T) with the rows' scales; Y fp32 or bf16."""
+    (M, K), N = a_codes.shape, b_codes.shape[0]
+    wp, wb = _ws(ws)
+    _check(LIB.int8_gemm(_buf(a_codes, "a_codes", (M, K), _I8), _buf(a_scales, "a_scales", (M,), _F32),
+                         _buf(b_codes, "b_codes", (N, K), _I8), _buf(b_scales, "b_scales", (N,), _F32), M, N, K,
+                         _buf(Y, "Y", (M, N)), _dt(Y.dtype), wp, wb, _stream(stream)), "int8_gemm")
 
 
 # ------------------------------------------------------------- weight container

@@ -45,18 +45,23 @@ __device__ __forceinline__ void adam_one(float& p, float g, float& m, float& v, 
 
 // Four elements per thread with 16-byte accesses, grid-stride; the last n % 4
 // elements one by one.
+// CLIP: the gradient is fl32(g *coef), coef from the gradient norm.
+template <bool CLIP>
 __global__ void __launch_bounds__(256) adamw_kernel(float* __restrict__ p, const float* __restrict__ g,
                                                     float* __restrict__ m, float* __restrict__ v,
-                                                    __nv_bfloat16* __restrict__ p_bf16, int64_t n, AdamConsts k) {
+                                                    __nv_bfloat16* __restrict__ p_bf16, int64_t n, AdamConsts k,
+                                                    const float* __restrict__ coef) {
   pdl_wait();
   pdl_trigger();
+  const float c = CLIP ? *coef : 1.0f;
   const int64_t n4 = n / 4;
   const int64_t stride = (int64_t)gridDim.x * blockDim.x;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n4; i += stride) {
     float4 P = reinterpret_cast<float4*>(p)[i];
-    const float4 G = reinterpret_cast<const float4*>(g)[i];
+    float4 G = reinterpret_cast<const float4*>(g)[i];
     float4 Mv = reinterpret_cast<float4*>(m)[i];
     float4 V = reinterpret_cast<float4*>(v)[i];
+    if (CLIP) G = make_float4(__fmul_rn(G.x, c), __fmul_rn(G.y, c), __fmul_rn(G.z, c), __fmul_rn(G.w, c));
     adam_one(P.x, G.x, Mv.x, V.x, k);
     adam_one(P.y, G.y, Mv.y, V.y, k);
     adam_one(P.z, G.z, Mv.z, V.z, k);
@@ -73,7 +78,7 @@ __global__ void __launch_bounds__(256) adamw_kernel(float* __restrict__ p, const
   }
   for (int64_t j = n4 * 4 + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; j < n; j += stride) {
     float P = p[j], Mv = m[j], V = v[j];
-    adam_one(P, g[j], Mv, V, k);
+    adam_one(P, CLIP ? __fmul_rn(g[j], c) : g[j], Mv, V, k);
     p[j] = P;
     m[j] = Mv;
     v[j] = V;
@@ -82,7 +87,7 @@ __global__ void __launch_bounds__(256) adamw_kernel(float* __restrict__ p, const
 }
 
 ql_status launch_adamw(float* p, const float* g, float* m, float* v, void* p_bf16, int64_t n, int64_t t, float lr,
-                       float b1, float b2, float eps, float wd, cudaStream_t st) {
+                       float b1, float b2, float eps, float wd, const float* coef, cudaStream_t st) {
   AdamConsts k;
   // host constants: float64 arithmetic on the fp32 inputs, one rounding each
   k.keep = (float)(1.0 - (double)lr * (double)wd);
@@ -98,8 +103,8 @@ ql_status launch_adamw(float* p, const float* g, float* m, float* v, void* p_bf1
   const int64_t need = (std::max<int64_t>(n / 4, 1) + 255) / 256;
   const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(need, (int64_t)sms * 8));
   TraceScope ts(TK_ADAMW, st);
-  QL_CUDA_TRY(launch(adamw_kernel, dim3(grid), dim3(256), 0, st, 1, 1, p, g, m, v,
-                     reinterpret_cast<__nv_bfloat16*>(p_bf16), n, k));
+  QL_CUDA_TRY(launch(coef ? adamw_kernel<true> : adamw_kernel<false>, dim3(grid), dim3(256), 0, st, 1, 1, p, g, m, v,
+                     reinterpret_cast<__nv_bfloat16*>(p_bf16), n, k, coef));
   QL_LAUNCH_CHECK();
   return QL_OK;
 }

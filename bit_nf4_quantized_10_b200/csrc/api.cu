@@ -61,8 +61,31 @@ ql_status launch_fp4_gemm(int vs, const uint8_t* a_codes, const uint8_t* a_atoms
                           int64_t K, float* Y, cudaStream_t st);
 // adamw.cu
 ql_status launch_adamw(float* p, const float* g, float* m, float* v, void* p_bf16, int64_t n, int64_t t, float lr,
-                       float b1, float b2, float eps, float wd, cudaStream_t st);
+                       float b1, float b2, float eps, float wd, const float* coef, cudaStream_t st);
 ql_status paged_prefetch(const void* ptr, size_t bytes, int where, cudaStream_t st);
+// gradnorm.cu
+unsigned status_word_gradnorm(cudaStream_t st);
+size_t grad_norm_ws(int64_t count);
+int64_t grad_list_max_values();
+ql_status launch_grad_norm(const ql_tensor_list* list, float max_norm, float* norm, float* coef, void* ws,
+                           cudaStream_t st);
+ql_status launch_grad_scale(const ql_tensor_list* list, const float* coef, cudaStream_t st);
+// norm.cu
+size_t block_norm_bwd_ws(int64_t M, int64_t D, int64_t gate_rows);
+ql_status launch_block_norm_fwd(const ql_block_norm* n, const void* x, ql_dtype x_dt, const void* h, ql_dtype h_dt,
+                                int64_t M, int64_t D, void* x_out, void* y, ql_dtype y_dt, float* rstd_pre,
+                                float* rstd_post, cudaStream_t st);
+ql_status launch_block_norm_bwd(const ql_block_norm* n, const void* x_out, ql_dtype x_dt, const void* h, ql_dtype h_dt,
+                                const float* rstd_pre, const float* rstd_post, const void* dx_out, const void* dy,
+                                ql_dtype dy_dt, int64_t M, int64_t D, void* dx, void* dh, float* dw_pre,
+                                float* dw_post, float* dgate, void* ws, cudaStream_t st);
+// int8.cu
+unsigned status_word_int8(cudaStream_t st);
+size_t int8_gemm_ws(int64_t M, int64_t N, int64_t K);
+ql_status launch_int8_quantize(const void* x, ql_dtype dt, int64_t rows, int64_t K, int8_t* codes, float* scales,
+                               cudaStream_t st);
+ql_status launch_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const float* sb, int64_t M, int64_t N,
+                           int64_t K, void* Y, ql_dtype y_dt, void* ws, cudaStream_t st);
 // mlp.cu
 ql_status launch_silu_gate_fwd(const void* g, const void* u, void* h, int64_t n, cudaStream_t st);
 ql_status launch_silu_gate_bwd(const void* dh, const void* g, const void* u, void* dg, void* du, int64_t n,
@@ -96,6 +119,39 @@ ql_status check_gemm_shape(const ql_nf4_weight* w, int64_t M, int r) {
   if (M >= (1ll << 31) || w->rows >= (1ll << 31) || w->cols >= (1ll << 31)) return QL_ERR_UNSUPPORTED;
   if (r < 0 || r % 8 != 0) return QL_ERR_INVALID_ARG;
   if (r > QL_MAX_RANK) return QL_ERR_UNSUPPORTED;
+  return QL_OK;
+}
+
+inline bool opt16(const void* p) { return !p || aligned16(p); }
+inline bool aligned4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+ql_status check_adamw(const float* p, const float* g, const float* m, const float* v, const void* p_bf16, int64_t n,
+                      int64_t t, float beta1, float beta2, float eps) {
+  if (n <= 0 || t < 1) return QL_ERR_INVALID_ARG;
+  if (!aligned16(p) || !aligned16(g) || !aligned16(m) || !aligned16(v) || !opt16(p_bf16)) return QL_ERR_INVALID_ARG;
+  if (!(beta1 >= 0.0f && beta1 < 1.0f) || !(beta2 >= 0.0f && beta2 < 1.0f) || !(eps >= 0.0f)) return QL_ERR_INVALID_ARG;
+  return QL_OK;
+}
+
+ql_status check_list(const ql_tensor_list* l) {
+  if (!l || l->count < 0) return QL_ERR_INVALID_ARG;
+  if (l->count > 0 && (!l->data || !l->numel || !l->dt)) return QL_ERR_INVALID_ARG;
+  for (int64_t i = 0; i < l->count; ++i) {
+    if (l->numel[i] < 0 || (l->dt[i] != QL_F32 && l->dt[i] != QL_BF16)) return QL_ERR_INVALID_ARG;
+    if (l->numel[i] > 0 && !aligned16(l->data[i])) return QL_ERR_INVALID_ARG;
+    if (l->numel[i] >= (int64_t)1 << 43) return QL_ERR_UNSUPPORTED;
+  }
+  return QL_OK;
+}
+
+// The parameters of a block norm; w_post and the gate count only with a block
+// output (or its gradient).
+ql_status check_norm(const ql_block_norm* n, int64_t M, int64_t D, bool branch) {
+  if (!n || M < 0 || D < 1 || !(n->eps >= 0.0f)) return QL_ERR_INVALID_ARG;
+  if ((n->w_pre || n->w_post || n->gate) && !dtype_ok(n->w_dt)) return QL_ERR_INVALID_ARG;
+  if (!opt16(n->w_pre)) return QL_ERR_INVALID_ARG;
+  if (branch && (!opt16(n->w_post) || !opt16(n->gate) || (n->gate && n->gate_rows < 1))) return QL_ERR_INVALID_ARG;
+  if (D > QL_MAX_NORM_DIM || M >= ((int64_t)1 << 31)) return QL_ERR_UNSUPPORTED;
   return QL_OK;
 }
 
@@ -363,11 +419,114 @@ ql_status mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_atoms, const uint8
 ql_status qlora_adamw_step(float* p, const float* g, float* m, float* v, void* p_bf16, int64_t n, int64_t t, float lr,
                            float beta1, float beta2, float eps, float weight_decay, void* stream) {
   NvtxRange nvtx_range("qlora_nf4/qlora_adamw_step");
-  if (n <= 0 || t < 1) return QL_ERR_INVALID_ARG;
-  if (!aligned16(p) || !aligned16(g) || !aligned16(m) || !aligned16(v) || (p_bf16 && !aligned16(p_bf16)))
+  ql_status st = check_adamw(p, g, m, v, p_bf16, n, t, beta1, beta2, eps);
+  if (st != QL_OK) return st;
+  return ql::launch_adamw(p, g, m, v, p_bf16, n, t, lr, beta1, beta2, eps, weight_decay, nullptr, as_stream(stream));
+}
+
+ql_status qlora_adamw_step_clipped(float* p, const float* g, float* m, float* v, void* p_bf16, int64_t n, int64_t t,
+                                   float lr, float beta1, float beta2, float eps, float weight_decay,
+                                   const float* coef, void* stream) {
+  NvtxRange nvtx_range("qlora_nf4/qlora_adamw_step_clipped");
+  ql_status st = check_adamw(p, g, m, v, p_bf16, n, t, beta1, beta2, eps);
+  if (st != QL_OK) return st;
+  if (!aligned4(coef)) return QL_ERR_INVALID_ARG;
+  return ql::launch_adamw(p, g, m, v, p_bf16, n, t, lr, beta1, beta2, eps, weight_decay, coef, as_stream(stream));
+}
+
+ql_status qlora_grad_norm(const ql_tensor_list* list, float max_norm, float* norm, float* coef, void* ws,
+                          size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_range("qlora_nf4/qlora_grad_norm");
+  ql_status st = check_list(list);
+  if (st != QL_OK) return st;
+  if (!(max_norm >= 0.0f) || (norm && !aligned4(norm)) || (coef && !aligned4(coef)) || !aligned16(ws))
     return QL_ERR_INVALID_ARG;
-  if (!(beta1 >= 0.0f && beta1 < 1.0f) || !(beta2 >= 0.0f && beta2 < 1.0f) || !(eps >= 0.0f)) return QL_ERR_INVALID_ARG;
-  return ql::launch_adamw(p, g, m, v, p_bf16, n, t, lr, beta1, beta2, eps, weight_decay, as_stream(stream));
+  if (ws_bytes < ql::grad_norm_ws(list->count)) return QL_ERR_WORKSPACE;
+  return ql::launch_grad_norm(list, max_norm, norm, coef, ws, as_stream(stream));
+}
+
+ql_status qlora_grad_scale(const ql_tensor_list* list, const float* coef, void* stream) {
+  NvtxRange nvtx_range("qlora_nf4/qlora_grad_scale");
+  ql_status st = check_list(list);
+  if (st != QL_OK) return st;
+  if (!aligned4(coef)) return QL_ERR_INVALID_ARG;
+  return ql::launch_grad_scale(list, coef, as_stream(stream));
+}
+
+ql_status qlora_block_norm_fwd(const ql_block_norm* norm, const void* x, ql_dtype x_dt, const void* h, ql_dtype h_dt,
+                               int64_t M, int64_t D, void* x_out, void* y, ql_dtype y_dt, float* rstd_pre,
+                               float* rstd_post, void* stream) {
+  NvtxRange nvtx_range("qlora_nf4/qlora_block_norm_fwd");
+  ql_status st = check_norm(norm, M, D, h != nullptr);
+  if (st != QL_OK) return st;
+  if (!dtype_ok(x_dt) || (h && !dtype_ok(h_dt)) || (y && !dtype_ok(y_dt))) return QL_ERR_INVALID_ARG;
+  if ((!x_out && !y) || (y && !norm->w_pre)) return QL_ERR_INVALID_ARG;
+  if (M == 0) return QL_OK;
+  if (!aligned16(x) || !opt16(h) || !opt16(x_out) || !opt16(y) || !opt16(rstd_pre) || !opt16(rstd_post))
+    return QL_ERR_INVALID_ARG;
+  return ql::launch_block_norm_fwd(norm, x, x_dt, h, h ? h_dt : x_dt, M, D, x_out, y, y_dt, rstd_pre, rstd_post,
+                                   as_stream(stream));
+}
+
+ql_status qlora_block_norm_bwd(const ql_block_norm* norm, const void* x_out, ql_dtype x_dt, const void* h,
+                               ql_dtype h_dt, const float* rstd_pre, const float* rstd_post, const void* dx_out,
+                               const void* dy, ql_dtype dy_dt, int64_t M, int64_t D, void* dx, void* dh,
+                               float* dw_pre, float* dw_post, float* dgate, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_range("qlora_nf4/qlora_block_norm_bwd");
+  // without h only the stream's gradient is left; dh then needs no h unless a norm or a sum reads it
+  const bool branch = h || dh;
+  ql_status st = check_norm(norm, M, D, branch);
+  if (st != QL_OK) return st;
+  if (!dtype_ok(x_dt) || (branch && !dtype_ok(h_dt)) || (dy && !dtype_ok(dy_dt))) return QL_ERR_INVALID_ARG;
+  if (!dx && !dh && !dw_pre && !dw_post && !dgate) return QL_ERR_INVALID_ARG;
+  if ((dw_pre && !aligned16(dw_pre)) || (dw_post && !aligned16(dw_post)) || (dgate && !aligned16(dgate)))
+    return QL_ERR_INVALID_ARG;
+  if (dgate && !norm->gate) return QL_ERR_INVALID_ARG;
+  if (dw_post && !norm->w_post) return QL_ERR_INVALID_ARG;
+  cudaStream_t cs = as_stream(stream);
+  if (M == 0) {
+    if (dw_pre) QL_CUDA_TRY(cudaMemsetAsync(dw_pre, 0, (size_t)D * 4, cs));
+    if (dw_post) QL_CUDA_TRY(cudaMemsetAsync(dw_post, 0, (size_t)D * 4, cs));
+    return QL_OK;
+  }
+  if (!dx_out && !dy) return QL_ERR_INVALID_ARG;
+  if (dy && (!norm->w_pre || !aligned16(dy) || !aligned16(x_out) || !aligned16(rstd_pre))) return QL_ERR_INVALID_ARG;
+  if (dw_pre && !dy) return QL_ERR_INVALID_ARG;
+  const bool read_h = (dh && norm->w_post) || dw_post || dgate;
+  if (read_h && !aligned16(h)) return QL_ERR_INVALID_ARG;
+  if (read_h && norm->w_post && !aligned16(rstd_post)) return QL_ERR_INVALID_ARG;
+  if (!opt16(dx_out) || !opt16(dx) || !opt16(dh)) return QL_ERR_INVALID_ARG;
+  if (dw_pre || dw_post || dgate) {
+    if (ws_bytes < ql::block_norm_bwd_ws(M, D, norm->gate ? norm->gate_rows : 0)) return QL_ERR_WORKSPACE;
+    if (!aligned16(ws)) return QL_ERR_INVALID_ARG;
+  }
+  return ql::launch_block_norm_bwd(norm, x_out, x_dt, read_h ? h : nullptr, branch ? h_dt : x_dt, rstd_pre, rstd_post,
+                                   dx_out, dy, dy_dt, M, D, dx, dh, dw_pre, dw_post, dgate, ws, cs);
+}
+
+ql_status int8_quantize(const void* x, ql_dtype x_dt, int64_t rows, int64_t K, int8_t* codes, float* scales,
+                        void* stream) {
+  NvtxRange nvtx_range("qlora_nf4/int8_quantize");
+  if (rows < 1 || K < 1 || !dtype_ok(x_dt)) return QL_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return QL_ERR_INVALID_ARG;
+  if (K % 16 != 0 || K > QL_MAX_INT8_K || rows >= ((int64_t)1 << 31)) return QL_ERR_UNSUPPORTED;
+  return ql::launch_int8_quantize(x, x_dt, rows, K, codes, scales, as_stream(stream));
+}
+
+ql_status int8_gemm(const int8_t* a, const float* a_scales, const int8_t* b, const float* b_scales, int64_t M,
+                    int64_t N, int64_t K, void* Y, ql_dtype y_dt, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_range("qlora_nf4/int8_gemm");
+  if (M < 0 || N < 1 || K < 1 || !dtype_ok(y_dt)) return QL_ERR_INVALID_ARG;
+  if (K % 16 != 0 || K > QL_MAX_INT8_K || M >= ((int64_t)1 << 31) || N >= ((int64_t)1 << 31) ||
+      ((M + 255) / 256) * ((N + 255) / 256) >= ((int64_t)1 << 30))
+    return QL_ERR_UNSUPPORTED;
+  if (M == 0) return QL_OK;
+  if (!aligned16(a) || !aligned16(a_scales) || !aligned16(b) || !aligned16(b_scales) || !aligned16(Y))
+    return QL_ERR_INVALID_ARG;
+  const size_t need = ql::int8_gemm_ws(M, N, K);
+  if (ws_bytes < need) return QL_ERR_WORKSPACE;
+  if (need && !aligned16(ws)) return QL_ERR_INVALID_ARG;
+  return ql::launch_int8_gemm(a, a_scales, b, b_scales, M, N, K, Y, y_dt, ws, as_stream(stream));
 }
 
 ql_status qlora_paged_prefetch(const void* ptr, size_t bytes, int where, void* stream) {
@@ -401,6 +560,9 @@ size_t qlora_workspace_size(int op, int64_t M, int64_t N, int64_t K, int r) {
     case QL_OP_FWD: return ws_fwd(M, N, K, r);
     case QL_OP_BWD: return ws_bwd(M, N, K, r);
     case QL_OP_NVFP4: return M > 0 ? 256 : 0;
+    case QL_OP_BLOCK_NORM_BWD: return ql::block_norm_bwd_ws(M, N, K);
+    case QL_OP_GRAD_NORM: return M >= 0 ? ql::grad_norm_ws(M) : 0;
+    case QL_OP_INT8_GEMM: return ql::int8_gemm_ws(M, N, K);
     default: return 0;
   }
 }
@@ -423,7 +585,7 @@ ql_status qlora_get_status(void* stream) {
   unsigned v = 0;
   for (unsigned (*word)(cudaStream_t) : {ql::status_word_codec, ql::status_word_gemm, ql::status_word_lora,
                                          ql::status_word_smallm, ql::status_word_diag, ql::status_word_fp4,
-                                         ql::status_word_fp4g}) {
+                                         ql::status_word_fp4g, ql::status_word_gradnorm, ql::status_word_int8}) {
     const unsigned w = word(cs);
     if (w == ~0u) return QL_ERR_CUDA;
     v |= w;

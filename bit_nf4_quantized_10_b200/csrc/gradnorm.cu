@@ -1,0 +1,267 @@
+// The global norm of a list of gradient tensors, the clipping coefficient, and
+// the clipping of the gradients in place:
+//   norm = sqrt(sum of g^2 over every value of every tensor)
+//   coef = min(1, max_norm / (norm + 1e-6)),   g = round(g coef)
+// Two operations a value: both kernels are bound by HBM (the norm reads every
+// gradient once; the scaling reads and writes it once).
+//
+// Squares are formed and summed in float64: a bf16 or fp32 value squared can
+// neither overflow nor vanish there, and a list of 10^9 values loses nothing.
+// Each block's sum goes to its own slot and one more block adds the slots in a
+// fixed order, so equal gradients give equal norms bit for bit (no atomics).
+//
+// The list travels as a kernel argument (up to kCap tensors a launch), so a
+// call copies nothing to the device and a captured graph keeps the list it was
+// captured with.
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+#include "trace.cuh"
+
+namespace ql {
+
+QL_DEFINE_STATUS_ACCESSOR(status_word_gradnorm)
+
+namespace gn {
+
+constexpr int kCap = 1024;       // tensors a launch: 20.5 KB of the 32 KB an argument list may have
+constexpr int kThreads = 256;
+constexpr int kChunk = 8192;     // values a block takes at a time
+
+// Chunks of all tensors are numbered in order; tensor i has chunks first[i] .. first[i + 1] - 1.
+template <int CAP>
+struct List {
+  uint64_t data[CAP];            // bit 0: the values are bf16 (addresses are multiples of 16)
+  int64_t numel[CAP];
+  uint32_t first[CAP + 1];
+  int count;
+};
+
+template <int CAP>
+__device__ __forceinline__ int tensor_of(const List<CAP>& l, uint32_t chunk) {
+  int lo = 0, hi = l.count - 1;  // the last tensor whose first chunk is <= chunk
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (l.first[mid] <= chunk) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ double sq(double acc, float v) {
+  const double d = v;
+  return fma(d, d, acc);
+}
+
+__device__ __forceinline__ double block_sum(double v, double* buf) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) v += buf[w];
+  return v;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) grad_sumsq_kernel(const __grid_constant__ List<CAP> l, double* parts) {
+  __shared__ double buf[kThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int t = threadIdx.x;
+  const uint32_t chunks = l.first[l.count];
+  double acc[4] = {0.0, 0.0, 0.0, 0.0};
+  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const int i = tensor_of(l, c);
+    const int64_t start = (int64_t)(c - l.first[i]) * kChunk;
+    const int64_t left = l.numel[i] - start;
+    const int len = left < kChunk ? (int)left : kChunk;
+    const bool is_bf16 = l.data[i] & 1;
+    if (is_bf16) {
+      const __nv_bfloat16* g = reinterpret_cast<const __nv_bfloat16*>(l.data[i] & ~(uint64_t)1) + start;
+      uint4 v[kChunk / 8 / kThreads];
+#pragma unroll
+      for (int k = 0; k < kChunk / 8 / kThreads; ++k) {
+        const int e = (k * kThreads + t) * 8;
+        v[k] = e + 8 <= len ? *reinterpret_cast<const uint4*>(g + e) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < kChunk / 8 / kThreads; ++k) {
+        acc[0] = sq(sq(acc[0], bf16_lo(v[k].x)), bf16_hi(v[k].x));
+        acc[1] = sq(sq(acc[1], bf16_lo(v[k].y)), bf16_hi(v[k].y));
+        acc[2] = sq(sq(acc[2], bf16_lo(v[k].z)), bf16_hi(v[k].z));
+        acc[3] = sq(sq(acc[3], bf16_lo(v[k].w)), bf16_hi(v[k].w));
+      }
+      const int tail = (len & ~7) + t;
+      if (tail < len) acc[0] = sq(acc[0], __bfloat162float(g[tail]));
+    } else {
+      const float* g = reinterpret_cast<const float*>(l.data[i]) + start;
+      float4 v[kChunk / 4 / kThreads];
+#pragma unroll
+      for (int k = 0; k < kChunk / 4 / kThreads; ++k) {
+        const int e = (k * kThreads + t) * 4;
+        v[k] = e + 4 <= len ? *reinterpret_cast<const float4*>(g + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < kChunk / 4 / kThreads; ++k) {
+        acc[0] = sq(acc[0], v[k].x);
+        acc[1] = sq(acc[1], v[k].y);
+        acc[2] = sq(acc[2], v[k].z);
+        acc[3] = sq(acc[3], v[k].w);
+      }
+      const int tail = (len & ~3) + t;
+      if (tail < len) acc[0] = sq(acc[0], g[tail]);
+    }
+  }
+  const double s = block_sum((acc[0] + acc[1]) + (acc[2] + acc[3]), buf);
+  if (t == 0) parts[blockIdx.x] = s;
+}
+
+__device__ __forceinline__ void write_norm(double sum, float max_norm, float* norm, float* coef) {
+  const float n = (float)sqrt(sum);
+  const float c = max_norm / (n + 1e-6f);
+  if (norm) *norm = n;
+  if (coef) *coef = c > 1.0f ? 1.0f : c;   // a NaN stays one
+  if (!isfinite(n)) raise_status(ST_NONFINITE);
+}
+
+__global__ void __launch_bounds__(kThreads) grad_norm_finish_kernel(const double* parts, int count, float max_norm,
+                                                                    float* norm, float* coef) {
+  __shared__ double buf[kThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  double v = 0.0;
+  for (int i = threadIdx.x; i < count; i += kThreads) v += parts[i];
+  v = block_sum(v, buf);
+  if (threadIdx.x == 0) write_norm(v, max_norm, norm, coef);
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ List<CAP> l, const float* coef) {
+  pdl_wait();
+  pdl_trigger();
+  const float s = *coef;
+  if (s == 1.0f) return;   // g 1 = g
+  const int t = threadIdx.x;
+  const uint32_t chunks = l.first[l.count];
+  // from the last chunk to the first: the norm read the last ones last, and L2 still holds them
+  for (uint32_t k0 = blockIdx.x; k0 < chunks; k0 += gridDim.x) {
+    const uint32_t c = chunks - 1 - k0;
+    const int i = tensor_of(l, c);
+    const int64_t start = (int64_t)(c - l.first[i]) * kChunk;
+    const int64_t left = l.numel[i] - start;
+    const int len = left < kChunk ? (int)left : kChunk;
+    if (l.data[i] & 1) {
+      __nv_bfloat16* g = reinterpret_cast<__nv_bfloat16*>(l.data[i] & ~(uint64_t)1) + start;
+      uint4 v[kChunk / 8 / kThreads];
+#pragma unroll
+      for (int k = 0; k < kChunk / 8 / kThreads; ++k) {
+        const int e = (k * kThreads + t) * 8;
+        if (e + 8 <= len) v[k] = *reinterpret_cast<const uint4*>(g + e);
+      }
+#pragma unroll
+      for (int k = 0; k < kChunk / 8 / kThreads; ++k) {
+        const int e = (k * kThreads + t) * 8;
+        if (e + 8 > len) continue;
+        uint4 o;
+        o.x = pack_bf16x2(bf16_lo(v[k].x) * s, bf16_hi(v[k].x) * s);
+        o.y = pack_bf16x2(bf16_lo(v[k].y) * s, bf16_hi(v[k].y) * s);
+        o.z = pack_bf16x2(bf16_lo(v[k].z) * s, bf16_hi(v[k].z) * s);
+        o.w = pack_bf16x2(bf16_lo(v[k].w) * s, bf16_hi(v[k].w) * s);
+        *reinterpret_cast<uint4*>(g + e) = o;
+      }
+      const int tail = (len & ~7) + t;
+      if (tail < len) g[tail] = __float2bfloat16_rn(__bfloat162float(g[tail]) * s);
+    } else {
+      float* g = reinterpret_cast<float*>(l.data[i]) + start;
+      float4 v[kChunk / 4 / kThreads];
+#pragma unroll
+      for (int k = 0; k < kChunk / 4 / kThreads; ++k) {
+        const int e = (k * kThreads + t) * 4;
+        if (e + 4 <= len) v[k] = *reinterpret_cast<const float4*>(g + e);
+      }
+#pragma unroll
+      for (int k = 0; k < kChunk / 4 / kThreads; ++k) {
+        const int e = (k * kThreads + t) * 4;
+        if (e + 4 > len) continue;
+        *reinterpret_cast<float4*>(g + e) = make_float4(v[k].x * s, v[k].y * s, v[k].z * s, v[k].w * s);
+      }
+      const int tail = (len & ~3) + t;
+      if (tail < len) g[tail] *= s;
+    }
+  }
+}
+
+// Blocks of a launch: 8 on each SM hold the memory pipe full.
+int max_blocks() { return (device_sm_count() > 0 ? device_sm_count() : 148) * 8; }
+
+// Fills `l` from tensor `at` on (empty tensors are left out) until it is full
+// or its chunks pass 2^31; returns the index after the last tensor taken.
+template <int CAP>
+int64_t fill(List<CAP>& l, const ql_tensor_list* in, int64_t at) {
+  int n = 0;
+  uint64_t chunks = 0;
+  for (; at < in->count && n < CAP; ++at) {
+    if (in->numel[at] == 0) continue;
+    const uint64_t add = (uint64_t)((in->numel[at] + kChunk - 1) / kChunk);
+    if (n > 0 && chunks + add > 0x7FFFFFFFu) break;
+    l.data[n] = (uint64_t)reinterpret_cast<uintptr_t>(in->data[at]) | (in->dt[at] == QL_BF16 ? 1u : 0u);
+    l.numel[n] = in->numel[at];
+    l.first[n] = (uint32_t)chunks;
+    chunks += add;
+    ++n;
+  }
+  l.count = n;
+  l.first[n] = (uint32_t)chunks;
+  return at;
+}
+
+}  // namespace gn
+
+// Slots for the blocks' sums: one launch for every kCap tensors (or 2^31
+// chunks, which a tensor of the largest size fills by itself).
+size_t grad_norm_ws(int64_t count) {
+  const int64_t launches = (count + gn::kCap - 1) / gn::kCap;
+  return (size_t)std::max<int64_t>(launches, 1) * gn::max_blocks() * sizeof(double);
+}
+
+int64_t grad_list_max_values() { return (int64_t)gn::kChunk * 0x7FFFFFFF; }
+
+ql_status launch_grad_norm(const ql_tensor_list* list, float max_norm, float* norm, float* coef, void* ws,
+                           cudaStream_t st) {
+  using namespace gn;
+  double* parts = reinterpret_cast<double*>(ws);
+  int used = 0;
+  List<kCap> l;
+  for (int64_t at = 0; at < list->count;) {
+    at = fill(l, list, at);
+    if (l.count == 0) break;
+    const unsigned grid = (unsigned)std::min<int64_t>(l.first[l.count], max_blocks());
+    TraceScope ts(TK_GRADNORM, st);
+    QL_CUDA_TRY(launch(grad_sumsq_kernel<kCap>, dim3(grid), dim3(kThreads), 0, st, 1, 1, l, parts + used));
+    QL_LAUNCH_CHECK();
+    used += (int)grid;
+  }
+  TraceScope ts(TK_GRADNORM, st);
+  QL_CUDA_TRY(launch(grad_norm_finish_kernel, dim3(1), dim3(kThreads), 0, st, 1, 1, (const double*)parts, used,
+                     max_norm, norm, coef));
+  QL_LAUNCH_CHECK();
+  return QL_OK;
+}
+
+ql_status launch_grad_scale(const ql_tensor_list* list, const float* coef, cudaStream_t st) {
+  using namespace gn;
+  List<kCap> l;
+  for (int64_t at = 0; at < list->count;) {
+    at = fill(l, list, at);
+    if (l.count == 0) break;
+    const unsigned grid = (unsigned)std::min<int64_t>(l.first[l.count], max_blocks());
+    TraceScope ts(TK_GRADNORM, st);
+    QL_CUDA_TRY(launch(grad_scale_kernel<kCap>, dim3(grid), dim3(kThreads), 0, st, 1, 1, l, coef));
+    QL_LAUNCH_CHECK();
+  }
+  return QL_OK;
+}
+
+}  // namespace ql

@@ -1,0 +1,724 @@
+// The norms before and after a block, fused with the block's gate and the
+// residual scale, forward and backward.  For a token row of D channels, with
+// o = w_offset, h the block's output and x the residual stream:
+//   nh = h rstd_h,  rstd_h = (mean h^2 + eps)^-1/2        (nh = h without w_post)
+//   x' = round(alpha x + gate[m / gate_rows] (o + w_post) nh)
+//   y  = round(x' rstd_x (o + w_pre)),  rstd_x = (mean x'^2 + eps)^-1/2
+// and, given the gradients dx' and dy,
+//   n  = x' rstd_x,  dn = dy (o + w_pre),  dr = dx' + rstd_x (dn - n mean(dn n))
+//   dx = alpha dr,   S = dr nh,   dnh = dr gate (o + w_post)
+//   dh = rstd_h (dnh - nh mean(dnh nh))                   (dh = dnh without w_post)
+//   dw_pre = sum_m dy n,  dgate = sum over the gate's rows of S (o + w_post),
+//   dw_post = sum_m gate S.
+// Every value is read once and written once; about 15 (forward) and 30
+// (backward) fp32 operations per element, so both directions are bound by HBM.
+//
+// Layout: the elements of all [M, D] tensors are taken in groups of 8 at flat
+// indexes that are multiples of 8 (16 bytes of bf16, 32 of fp32), whatever D
+// is.  A row of a D that is no multiple of 8 starts and ends inside a group;
+// only those edge groups are accessed element by element.
+#include <algorithm>
+
+#include "common.cuh"
+#include "trace.cuh"
+
+namespace ql {
+namespace bn {
+
+constexpr int kMaxD = 16384;      // widest row a block of kMaxThreads holds in registers
+constexpr int kMaxThreads = 544;  // 17 warps: 2049 groups (D = 16383 off a group boundary) in 4 per thread
+
+using bf16 = __nv_bfloat16;
+
+// Eight consecutive values, as loaded.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<bf16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const bf16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void to_f32(float (&v)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(w[i]);
+      v[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void to_f32(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(bf16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ float rounded(float v, const float*) { return v; }
+__device__ __forceinline__ float rounded(float v, const bf16*) { return __bfloat162float(__float2bfloat16_rn(v)); }
+
+// Columns c .. c+7 of a row (`row` points at its column 0); columns outside
+// [0, D) read as 0.  `full`: all eight are inside and the address is aligned.
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int c, int D, bool full, float (&v)[8]) {
+  if (full) {
+    Raw8<T> r;
+    r.load(row + c);
+    r.to_f32(v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (c + j >= 0 && c + j < D) ? to_f32(row[c + j]) : 0.0f;
+  }
+}
+
+__device__ __forceinline__ void store8_full(bf16* p, const float (&v)[8]) {
+  uint4 o;
+  o.x = pack_bf16x2(v[0], v[1]);
+  o.y = pack_bf16x2(v[2], v[3]);
+  o.z = pack_bf16x2(v[4], v[5]);
+  o.w = pack_bf16x2(v[6], v[7]);
+  *reinterpret_cast<uint4*>(p) = o;
+}
+__device__ __forceinline__ void store8_full(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* row, int c, int D, bool full, const float (&v)[8]) {
+  if (full) {
+    store8_full(row + c, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j >= 0 && c + j < D) put(row + c + j, v[j]);
+  }
+}
+
+// A weight or gate row of either type: values off + w[c .. c+7] (off alone, or
+// `off` for a NULL w; 0 outside the row).  The row itself starts on 16 bytes
+// only where D is a multiple of 8 (`vec`).
+__device__ __forceinline__ void loadw8(const void* w, bool f32, int64_t base, int c, int D, bool vec, float off,
+                                       float (&v)[8]) {
+  if (!w) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = off;
+    return;
+  }
+  if (f32)
+    load8(reinterpret_cast<const float*>(w) + base, c, D, vec, v);
+  else
+    load8(reinterpret_cast<const bf16*>(w) + base, c, D, vec, v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] += off;
+}
+
+// Sums of K values over the block (every thread gets them), one barrier: the
+// warps' sums go through buf[K][32], which the caller alternates between two
+// buffers so that a slow warp still reads the previous sums.
+template <int K>
+__device__ __forceinline__ void block_sums(float (&s)[K], float* buf) {
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], d);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) buf[k * 32 + warp] = s[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    s[k] = lane < warps ? buf[k * 32 + lane] : 0.0f;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], d);
+  }
+}
+template <int K>
+__device__ __forceinline__ void warp_sums(float (&s)[K]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], d);
+}
+
+struct FwdArgs {
+  const void* x;
+  const void* h;
+  void* x_out;
+  void* y;
+  float* rstd_pre;
+  float* rstd_post;
+  const void* w_pre;
+  const void* w_post;
+  const void* gate;
+  int64_t M, gate_rows;
+  int D;
+  float alpha, eps, offset;
+  bool w_f32, y_f32;
+};
+
+// One row per block (or, WARP, one per warp), held in registers as VPT groups
+// of 8 per thread.  GROUPED: D is a multiple of 8, so every group is whole.
+template <typename XT, typename HT, int VPT, bool GROUPED, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : kMaxThreads) norm_fwd_kernel(const FwdArgs a) {
+  __shared__ float red[2][32];
+  pdl_wait();
+  pdl_trigger();
+  const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
+  const int nt = WARP ? 32 : blockDim.x;
+  const int64_t m = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+  if (m >= a.M) return;   // WARP only: a whole warp
+  const int D = a.D;
+  const int64_t flat = m * D;
+  const int shift = GROUPED ? 0 : (int)(flat & 7);
+  const XT* x = reinterpret_cast<const XT*>(a.x) + flat;
+  const HT* h = reinterpret_cast<const HT*>(a.h) + flat;
+
+  float r[VPT][8], hv[VPT][8];
+  bool full[VPT];
+  int col[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    col[v] = (t + v * nt) * 8 - shift;
+    full[v] = col[v] >= 0 && col[v] + 8 <= D;
+    if (col[v] < D) {
+      load8(x, col[v], D, full[v], r[v]);
+      if (a.h) load8(h, col[v], D, full[v], hv[v]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[v][j] = hv[v][j] = 0.0f;
+    }
+  }
+  if (a.h) {
+    float rs = 1.0f;
+    if (a.w_post) {
+      float s[1] = {0.0f};
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[0] += hv[v][j] * hv[v][j];
+      if (WARP) warp_sums(s); else block_sums(s, red[0]);
+      rs = 1.0f / sqrtf(s[0] / (float)D + a.eps);
+      if (t == 0 && a.rstd_post) a.rstd_post[m] = rs;
+    }
+    const int64_t grow = a.gate ? (m / a.gate_rows) * D : 0;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      if (col[v] >= D) continue;
+      float wv[8], gv[8];
+      loadw8(a.w_post, a.w_f32, 0, col[v], D, GROUPED, a.w_post ? a.offset : 1.0f, wv);
+      loadw8(a.gate, a.w_f32, grow, col[v], D, GROUPED, a.gate ? 0.0f : 1.0f, gv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[v][j] = a.alpha * r[v][j] + gv[j] * (hv[v][j] * rs * wv[j]);
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[v][j] *= a.alpha;
+  }
+  // the norm reads the stream as it is stored
+  float s[1] = {0.0f};
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const bool in = col[v] < D;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      r[v][j] = rounded(r[v][j], (const XT*)nullptr);
+      if (in && (GROUPED || full[v] || (col[v] + j >= 0 && col[v] + j < D))) s[0] += r[v][j] * r[v][j];
+    }
+    if (in && a.x_out) store8(reinterpret_cast<XT*>(a.x_out) + flat, col[v], D, full[v], r[v]);
+  }
+  if (!a.y) return;
+  if (WARP) warp_sums(s); else block_sums(s, red[1]);
+  const float rs = 1.0f / sqrtf(s[0] / (float)D + a.eps);
+  if (t == 0 && a.rstd_pre) a.rstd_pre[m] = rs;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    if (col[v] >= D) continue;
+    float wv[8];
+    loadw8(a.w_pre, a.w_f32, 0, col[v], D, GROUPED, a.offset, wv);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) wv[j] *= r[v][j] * rs;
+    if (a.y_f32)
+      store8(reinterpret_cast<float*>(a.y) + flat, col[v], D, full[v], wv);
+    else
+      store8(reinterpret_cast<bf16*>(a.y) + flat, col[v], D, full[v], wv);
+  }
+}
+
+// ------------------------------------------------------------------ backward
+// Rows are dealt to the blocks in chunks that lie inside one gate's rows, so
+// that S (the sum of dr nh over the rows of a gate) is complete, or one part
+// of `per_group`, whenever a chunk ends.  Column sums are kept in shared
+// memory while a block works and leave it as one part per block; a second
+// kernel adds the parts in a fixed order (no atomics: the same inputs always
+// give the same gradients).
+struct BwdPlan {
+  int blocks;          // blocks of the main kernel
+  int64_t groups;      // gates (1 without)
+  int64_t group_rows;  // rows of one gate
+  int64_t per_group;   // chunks of one gate's rows
+  int64_t chunk_rows;
+  int64_t chunks;
+};
+
+struct BwdArgs {
+  const void* x;        // the stream after the block, as stored
+  const void* h;
+  const void* dx_out;
+  const void* dy;
+  void* dx;
+  void* dh;
+  const float* rstd_pre;
+  const float* rstd_post;
+  const void* w_pre;
+  const void* w_post;
+  const void* gate;
+  float* dgate;         // written here when a gate's rows are one chunk
+  float* part_pre;      // [blocks][D], or NULL
+  float* part_post;     // [blocks][D], or NULL
+  float* part_s;        // [chunks][D], or NULL
+  int64_t M;
+  int D;
+  float alpha, offset;
+  bool w_f32, post, load_h;
+  BwdPlan plan;
+};
+
+// Where column c's sum is kept.  GROUPED: groups of 8 as two halves of four, so
+// that a thread's two 16-byte accesses meet no bank conflict.  Otherwise
+// neighbouring threads hold columns 8 apart: columns with equal c % 8 are
+// neighbours.
+template <bool GROUPED>
+__device__ __forceinline__ int sum_at(int c, int D) {
+  const int groups = (D + 7) >> 3;
+  return GROUPED ? ((c >> 2) & 1) * groups * 4 + (c >> 3) * 4 + (c & 3) : (c & 7) * groups + (c >> 3);
+}
+
+template <bool GROUPED>
+__device__ __forceinline__ void add_sums(float* acc, int c, int D, const float (&v)[8]) {
+  if (GROUPED) {
+    float4* p0 = reinterpret_cast<float4*>(acc + sum_at<true>(c, D));
+    float4* p1 = reinterpret_cast<float4*>(acc + sum_at<true>(c + 4, D));
+    float4 a = *p0, b = *p1;
+    a.x += v[0]; a.y += v[1]; a.z += v[2]; a.w += v[3];
+    b.x += v[4]; b.y += v[5]; b.z += v[6]; b.w += v[7];
+    *p0 = a;
+    *p1 = b;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j >= 0 && c + j < D) acc[sum_at<false>(c + j, D)] += v[j];
+  }
+}
+
+template <typename XT, typename HT, typename YT, int VPT, bool GROUPED>
+__global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const BwdArgs a) {
+  extern __shared__ __align__(16) float sums[];
+  __shared__ float red[2][3 * 32];
+  pdl_wait();
+  pdl_trigger();
+  const int t = threadIdx.x, nt = blockDim.x, D = a.D;
+  const int sum_len = (D + 7) / 8 * 8;
+  const bool sum_s = a.part_post || a.part_s || a.dgate;
+  float* acc_pre = sums;                                          // sum dy n
+  float* acc_s = acc_pre + (a.part_pre ? sum_len : 0);            // sum dr nh
+  float* acc_post = acc_s + (sum_s ? sum_len : 0);                // sum gate S, when there is a gate
+  {
+    const int total = ((a.part_pre ? 1 : 0) + (sum_s ? 1 : 0) + (a.part_post && a.gate ? 1 : 0)) * sum_len;
+    for (int i = t; i < total; i += nt) sums[i] = 0.0f;
+    __syncthreads();
+  }
+  int parity = 0;
+  for (int64_t chunk = blockIdx.x; chunk < a.plan.chunks; chunk += gridDim.x) {
+    const int64_t grp = chunk / a.plan.per_group;
+    const int64_t group_end = min(a.M, (grp + 1) * a.plan.group_rows);
+    const int64_t row0 = grp * a.plan.group_rows + (chunk % a.plan.per_group) * a.plan.chunk_rows;
+    const int64_t row1 = min(group_end, row0 + a.plan.chunk_rows);
+    const int64_t grow = grp * D;
+    for (int64_t m = row0; m < row1; ++m) {
+      const int64_t flat = m * D;
+      const int shift = GROUPED ? 0 : (int)(flat & 7);
+      float n[VPT][8], u[VPT][8], nh[VPT][8], gw[VPT][8];
+      const float rsx = a.dy ? a.rstd_pre[m] : 0.0f;
+      const float rsh = a.post ? a.rstd_post[m] : 1.0f;
+      float s[3] = {0.0f, 0.0f, 0.0f};   // sum dn n, sum u q, sum n q  with q = gate (o + w_post) nh
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int c = (t + v * nt) * 8 - shift;
+        const bool full = c >= 0 && c + 8 <= D;
+        if (c >= D) continue;
+        float dy[8];
+        if (a.dy) {
+          load8(reinterpret_cast<const XT*>(a.x) + flat, c, D, full, n[v]);
+          load8(reinterpret_cast<const YT*>(a.dy) + flat, c, D, full, dy);
+        }
+        if (a.dx_out) load8(reinterpret_cast<const XT*>(a.dx_out) + flat, c, D, full, u[v]);
+        else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[v][j] = 0.0f;
+        }
+        if (a.load_h) load8(reinterpret_cast<const HT*>(a.h) + flat, c, D, full, nh[v]);
+        else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) nh[v][j] = 0.0f;
+        }
+        float w[8];
+        if (a.dh) {
+          loadw8(a.w_post, a.w_f32, 0, c, D, GROUPED, a.w_post ? a.offset : 1.0f, w);
+          loadw8(a.gate, a.w_f32, grow, c, D, GROUPED, a.gate ? 0.0f : 1.0f, gw[v]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) gw[v][j] *= w[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) gw[v][j] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) nh[v][j] *= rsh;
+        if (a.dy) {
+          loadw8(a.w_pre, a.w_f32, 0, c, D, GROUPED, a.offset, w);
+          float dyn[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            n[v][j] *= rsx;
+            dyn[j] = dy[j] * n[v][j];
+            const float dn = dy[j] * w[j];
+            u[v][j] += rsx * dn;
+            s[0] += dn * n[v][j];
+          }
+          if (a.part_pre) add_sums<GROUPED>(acc_pre, c, D, dyn);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) n[v][j] = 0.0f;
+        }
+        if (a.post) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float qv = gw[v][j] * nh[v][j];
+            s[1] += u[v][j] * qv;
+            s[2] += n[v][j] * qv;
+          }
+        }
+      }
+      // dr = u - rsx c1 n with c1 = mean(dn n), so mean(dnh nh) = mean(u q) - rsx c1 mean(n q)
+      block_sums(s, red[parity]);
+      parity ^= 1;
+      const float k1 = rsx * (s[0] / (float)D);
+      const float c2 = (s[1] - k1 * s[2]) / (float)D;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int c = (t + v * nt) * 8 - shift;
+        const bool full = c >= 0 && c + 8 <= D;
+        if (c >= D) continue;
+        float o[8], sv[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          u[v][j] -= k1 * n[v][j];       // dr
+          o[j] = a.alpha * u[v][j];
+          sv[j] = u[v][j] * nh[v][j];
+        }
+        if (a.dx) store8(reinterpret_cast<XT*>(a.dx) + flat, c, D, full, o);
+        if (sum_s) add_sums<GROUPED>(acc_s, c, D, sv);
+        if (a.dh) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            o[j] = u[v][j] * gw[v][j];
+            if (a.post) o[j] = rsh * (o[j] - nh[v][j] * c2);
+          }
+          store8(reinterpret_cast<HT*>(a.dh) + flat, c, D, full, o);
+        }
+      }
+    }
+    if (sum_s && a.gate) {
+      __syncthreads();
+      for (int c = t; c < D; c += nt) {
+        const int i = sum_at<GROUPED>(c, D);
+        const float sv = acc_s[i];
+        acc_s[i] = 0.0f;
+        if (a.part_post) {
+          const float g = a.w_f32 ? reinterpret_cast<const float*>(a.gate)[grow + c]
+                                  : to_f32(reinterpret_cast<const bf16*>(a.gate)[grow + c]);
+          acc_post[i] += g * sv;
+        }
+        if (a.part_s) {
+          a.part_s[chunk * D + c] = sv;
+        } else if (a.dgate) {
+          const float w = !a.w_post ? 1.0f
+                          : a.offset + (a.w_f32 ? reinterpret_cast<const float*>(a.w_post)[c]
+                                                : to_f32(reinterpret_cast<const bf16*>(a.w_post)[c]));
+          a.dgate[grow + c] = w * sv;
+        }
+      }
+      __syncthreads();
+    }
+  }
+  if (a.part_pre || a.part_post) {
+    __syncthreads();
+    const float* post = a.gate ? acc_post : acc_s;
+    for (int c = t; c < D; c += nt) {
+      const int i = sum_at<GROUPED>(c, D);
+      if (a.part_pre) a.part_pre[(int64_t)blockIdx.x * D + c] = acc_pre[i];
+      if (a.part_post) a.part_post[(int64_t)blockIdx.x * D + c] = post[i];
+    }
+  }
+}
+
+// Adds the parts: 32 columns per block, its 8 warps take every 8th part each
+// and are added in order.  blockIdx.y: 0 dw_pre, 1 dw_post, 2 + g the gate g.
+struct FinishArgs {
+  const float* part_pre;
+  const float* part_post;
+  const float* part_s;
+  float* dw_pre;
+  float* dw_post;
+  float* dgate;
+  const void* w_post;
+  int blocks;
+  int64_t per_group;
+  int D;
+  float offset;
+  bool w_f32;
+};
+
+__global__ void __launch_bounds__(256) norm_finish_kernel(const FinishArgs a) {
+  __shared__ float part[8][32];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  const float* src = blockIdx.y == 0 ? a.part_pre : a.part_post;
+  float* dst = blockIdx.y == 0 ? a.dw_pre : a.dw_post;
+  int64_t parts = a.blocks;
+  float scale = 1.0f;
+  if (blockIdx.y >= 2) {
+    const int64_t g = blockIdx.y - 2;
+    src = a.part_s + g * a.per_group * a.D;
+    dst = a.dgate + g * a.D;
+    parts = a.per_group;
+    if (a.w_post && c < a.D)
+      scale = a.offset + (a.w_f32 ? reinterpret_cast<const float*>(a.w_post)[c]
+                                  : to_f32(reinterpret_cast<const bf16*>(a.w_post)[c]));
+  }
+  if (!src) return;
+  float s = 0.0f;
+  if (c < a.D)
+    for (int64_t p = warp; p < parts; p += 8) s += src[p * a.D + c];
+  part[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < a.D) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) s += part[w][lane];
+    dst[c] = s * scale;
+  }
+}
+
+// ---------------------------------------------------------------- host side
+// Groups of 8 that a row can touch.
+int row_groups(int64_t D) { return (int)(D % 8 ? (D + 7) / 8 + 1 : D / 8); }
+
+// Groups per thread: as few as a block of kMaxThreads allows.
+int groups_per_thread(int64_t D) {
+  const int g = row_groups(D);
+  return g <= 512 ? 1 : g <= 1024 ? 2 : 4;
+}
+unsigned row_threads(int64_t D, int vpt) { return (unsigned)((row_groups(D) + vpt * 32 - 1) / (vpt * 32) * 32); }
+
+BwdPlan bwd_plan(int64_t M, int64_t D, int64_t gate_rows) {
+  BwdPlan p;
+  p.group_rows = gate_rows > 0 && gate_rows < M ? gate_rows : M;
+  p.groups = (M + p.group_rows - 1) / p.group_rows;
+  const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
+  const int threads = (int)row_threads(D, groups_per_thread(D));
+  const int per_sm = std::max(1, std::min(8, 640 / threads));
+  const int64_t want = std::min<int64_t>(M, (int64_t)sms * per_sm);
+  // Chunks per gate: the count whose slowest block has the fewest rows to go
+  // through, a gate's chunk end counted as one row, over 1 to 8 chunks a block.
+  int64_t best = -1;
+  for (int waves = 1; waves <= 8; ++waves) {
+    const int64_t per = std::max<int64_t>(1, std::min(p.group_rows, waves * want / p.groups));
+    const int64_t rows = (p.group_rows + per - 1) / per;
+    const int64_t cost = (p.groups * per + want - 1) / want * (rows + (gate_rows > 0 ? 1 : 0));
+    if (best < 0 || cost < best) {
+      best = cost;
+      p.per_group = per;
+      p.chunk_rows = rows;
+    }
+  }
+  p.chunks = p.groups * p.per_group;
+  p.blocks = (int)std::min<int64_t>(want, p.chunks);
+  return p;
+}
+
+size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+template <typename XT, typename HT, int VPT, bool GROUPED, bool WARP>
+ql_status run_fwd(const FwdArgs& a, cudaStream_t st) {
+  const unsigned threads = WARP ? 256u : row_threads(a.D, VPT);
+  const int64_t grid = WARP ? (a.M + 7) / 8 : a.M;
+  TraceScope ts(TK_NORM, st);
+  QL_CUDA_TRY(launch(norm_fwd_kernel<XT, HT, VPT, GROUPED, WARP>, dim3((unsigned)grid), dim3(threads), 0, st, 1, 1, a));
+  QL_LAUNCH_CHECK();
+  return QL_OK;
+}
+
+template <typename XT, typename HT, bool GROUPED>
+ql_status pick_fwd(const FwdArgs& a, cudaStream_t st) {
+  // rows of up to 128 groups: one warp each, no block barrier
+  if (row_groups(a.D) <= 128) return run_fwd<XT, HT, 4, GROUPED, true>(a, st);
+  switch (groups_per_thread(a.D)) {
+    case 1: return run_fwd<XT, HT, 1, GROUPED, false>(a, st);
+    case 2: return run_fwd<XT, HT, 2, GROUPED, false>(a, st);
+    default: return run_fwd<XT, HT, 4, GROUPED, false>(a, st);
+  }
+}
+
+template <typename XT, typename HT, typename YT, int VPT, bool GROUPED>
+ql_status run_bwd(const BwdArgs& a, size_t smem, cudaStream_t st) {
+  const auto kernel = norm_bwd_kernel<XT, HT, YT, VPT, GROUPED>;
+  if (per_device(reinterpret_cast<const void*>(kernel), 0, [kernel] {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * 4 * kMaxD) != cudaSuccess) {
+          cudaGetLastError();
+          return -1;
+        }
+        return 1;
+      }) < 0)
+    return QL_ERR_CUDA;
+  TraceScope ts(TK_NORM, st);
+  QL_CUDA_TRY(launch(kernel, dim3((unsigned)a.plan.blocks), dim3(row_threads(a.D, VPT)), smem, st, 1, 1, a));
+  QL_LAUNCH_CHECK();
+  return QL_OK;
+}
+
+template <typename XT, typename HT, typename YT, bool GROUPED>
+ql_status pick_bwd(const BwdArgs& a, size_t smem, cudaStream_t st) {
+  switch (groups_per_thread(a.D)) {
+    case 1: return run_bwd<XT, HT, YT, 1, GROUPED>(a, smem, st);
+    case 2: return run_bwd<XT, HT, YT, 2, GROUPED>(a, smem, st);
+    default: return run_bwd<XT, HT, YT, 4, GROUPED>(a, smem, st);
+  }
+}
+
+template <typename XT, typename HT>
+ql_status pick_bwd_y(const BwdArgs& a, bool y_f32, size_t smem, cudaStream_t st) {
+  if (y_f32)
+    return a.D % 8 ? pick_bwd<XT, HT, float, false>(a, smem, st) : pick_bwd<XT, HT, float, true>(a, smem, st);
+  return a.D % 8 ? pick_bwd<XT, HT, bf16, false>(a, smem, st) : pick_bwd<XT, HT, bf16, true>(a, smem, st);
+}
+
+}  // namespace bn
+
+int64_t block_norm_max_d() { return bn::kMaxD; }
+
+// Parts of the column sums, carved in this order (each piece 256-byte aligned):
+//   dw_pre [blocks, D], dw_post [blocks, D], S [chunks, D] (gates of several chunks).
+size_t block_norm_bwd_ws(int64_t M, int64_t D, int64_t gate_rows) {
+  if (M <= 0 || D <= 0 || D > bn::kMaxD || gate_rows < 0) return 0;
+  const bn::BwdPlan p = bn::bwd_plan(M, D, gate_rows);
+  size_t b = 2 * bn::align256((size_t)p.blocks * D * 4);
+  if (gate_rows > 0 && p.per_group > 1) b += bn::align256((size_t)p.chunks * D * 4);
+  return b;
+}
+
+ql_status launch_block_norm_fwd(const ql_block_norm* n, const void* x, ql_dtype x_dt, const void* h, ql_dtype h_dt,
+                                int64_t M, int64_t D, void* x_out, void* y, ql_dtype y_dt, float* rstd_pre,
+                                float* rstd_post, cudaStream_t st) {
+  using namespace bn;
+  FwdArgs a;
+  a.x = x;
+  a.h = h;
+  a.x_out = x_out;
+  a.y = y;
+  a.rstd_pre = rstd_pre;
+  a.rstd_post = rstd_post;
+  a.w_pre = n->w_pre;
+  a.w_post = n->w_post;
+  a.gate = n->gate;
+  a.M = M;
+  a.gate_rows = n->gate_rows;
+  a.D = (int)D;
+  a.alpha = n->alpha;
+  a.eps = n->eps;
+  a.offset = n->w_offset;
+  a.w_f32 = n->w_dt == QL_F32;
+  a.y_f32 = y_dt == QL_F32;
+  const bool g = D % 8 == 0;
+  if (x_dt == QL_F32) {
+    if (h_dt == QL_F32) return g ? pick_fwd<float, float, true>(a, st) : pick_fwd<float, float, false>(a, st);
+    return g ? pick_fwd<float, bf16, true>(a, st) : pick_fwd<float, bf16, false>(a, st);
+  }
+  if (h_dt == QL_F32) return g ? pick_fwd<bf16, float, true>(a, st) : pick_fwd<bf16, float, false>(a, st);
+  return g ? pick_fwd<bf16, bf16, true>(a, st) : pick_fwd<bf16, bf16, false>(a, st);
+}
+
+ql_status launch_block_norm_bwd(const ql_block_norm* n, const void* x_out, ql_dtype x_dt, const void* h, ql_dtype h_dt,
+                                const float* rstd_pre, const float* rstd_post, const void* dx_out, const void* dy,
+                                ql_dtype dy_dt, int64_t M, int64_t D, void* dx, void* dh, float* dw_pre,
+                                float* dw_post, float* dgate, void* ws, cudaStream_t st) {
+  using namespace bn;
+  BwdArgs a;
+  a.plan = bwd_plan(M, D, n->gate ? n->gate_rows : 0);
+  const size_t part = align256((size_t)a.plan.blocks * D * 4);
+  uint8_t* wp = reinterpret_cast<uint8_t*>(ws);
+  a.part_pre = dw_pre ? reinterpret_cast<float*>(wp) : nullptr;
+  a.part_post = dw_post ? reinterpret_cast<float*>(wp + part) : nullptr;
+  a.part_s = dgate && a.plan.per_group > 1 ? reinterpret_cast<float*>(wp + 2 * part) : nullptr;
+  a.x = x_out;
+  a.h = h;
+  a.dx_out = dx_out;
+  a.dy = dy;
+  a.dx = dx;
+  a.dh = dh;
+  a.rstd_pre = rstd_pre;
+  a.rstd_post = rstd_post;
+  a.w_pre = n->w_pre;
+  a.w_post = n->w_post;
+  a.gate = n->gate;
+  a.dgate = dgate;
+  a.M = M;
+  a.D = (int)D;
+  a.alpha = n->alpha;
+  a.offset = n->w_offset;
+  a.w_f32 = n->w_dt == QL_F32;
+  a.post = h && n->w_post;
+  a.load_h = (dh && a.post) || dw_post || dgate;
+  const int64_t len = (D + 7) / 8 * 8;
+  const size_t smem = (size_t)len * 4 * ((dw_pre ? 1 : 0) + (dw_post || dgate ? 1 : 0) + (dw_post && n->gate ? 1 : 0));
+  const bool yf = dy && dy_dt == QL_F32;
+  ql_status rc;
+  if (x_dt == QL_F32)
+    rc = h_dt == QL_F32 ? pick_bwd_y<float, float>(a, yf, smem, st) : pick_bwd_y<float, bf16>(a, yf, smem, st);
+  else
+    rc = h_dt == QL_F32 ? pick_bwd_y<bf16, float>(a, yf, smem, st) : pick_bwd_y<bf16, bf16>(a, yf, smem, st);
+  if (rc != QL_OK || !(a.part_pre || a.part_post || a.part_s)) return rc;
+  FinishArgs f;
+  f.part_pre = a.part_pre;
+  f.part_post = a.part_post;
+  f.part_s = a.part_s;
+  f.dw_pre = dw_pre;
+  f.dw_post = dw_post;
+  f.dgate = dgate;
+  f.w_post = n->w_post;
+  f.blocks = a.plan.blocks;
+  f.per_group = a.plan.per_group;
+  f.D = (int)D;
+  f.offset = n->w_offset;
+  f.w_f32 = a.w_f32;
+  const dim3 grid((unsigned)((D + 31) / 32), 2u + (a.part_s ? (unsigned)a.plan.groups : 0u));
+  TraceScope ts(TK_NORM, st);
+  QL_CUDA_TRY(launch(norm_finish_kernel, grid, dim3(256), 0, st, 1, 1, f));
+  QL_LAUNCH_CHECK();
+  return QL_OK;
+}
+
+}  // namespace ql

@@ -27,6 +27,10 @@ enum TraceKind : int {
   TK_FP4,
   TK_ADAMW,
   TK_FP4GEMM,
+  TK_NORM,
+  TK_GRADNORM,
+  TK_INT8,
+  TK_INT8GEMM,
   TK_COUNT
 };
 

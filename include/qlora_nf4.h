@@ -400,11 +400,146 @@ ql_status qlora_adamw_step(float* p, const float* g, float* m, float* v, void* p
                            float lr, float beta1, float beta2, float eps, float weight_decay, void* stream);
 ql_status qlora_paged_prefetch(const void* ptr, size_t bytes, int where, void* stream);
 
+/*
+ * The global norm of the gradients and clipping, between the backward pass and
+ * the optimizer step.  The pages have no counterpart (they name the optimizer
+ * only); the formulas are
+ *   norm = sqrt(sum of g^2 over every value of every tensor of the list)
+ *   coef = min(1, max_norm / (norm + 1e-6)),  g = round(fl32(g coef)).
+ *
+ * ql_tensor_list: `count` tensors; data[i] device pointer (16-byte aligned) to
+ *   numel[i] >= 0 contiguous values of type dt[i]; data[i] is not looked at
+ *   where numel[i] == 0.  The three arrays are host memory, read during the
+ *   call only.  count == 0 is a list without values (norm 0).
+ * qlora_grad_norm: norm device out fp32 [1], coef device out fp32 [1]; either
+ *   may be NULL.  max_norm >= 0 (infinity: coef is 1).  Squares are summed in
+ *   float64 in a fixed order, so equal gradients give equal bits; norm = fl32(
+ *   sqrt(sum)), the other two operations are single fp32 operations.  A norm
+ *   that is not finite sets QL_ERR_NONFINITE in the status word; coef is then 0
+ *   (infinite norm) or NaN.  ws >= qlora_workspace_size(QL_OP_GRAD_NORM, count, 0, 0, 0).
+ * qlora_grad_scale: multiplies every value in place by *coef (device fp32 [1],
+ *   4-byte aligned); a coef of 1 leaves the tensors untouched.  A tensor must
+ *   not be listed twice nor overlap another.
+ * qlora_adamw_step_clipped: qlora_adamw_step with g replaced by fl32(g *coef)
+ *   (coef device fp32 [1], 4-byte aligned), so that clipping takes no pass of
+ *   its own; g itself is only read.
+ * Errors: QL_ERR_INVALID_ARG (a NULL list or array, count or numel < 0, an
+ * unknown dtype, a NULL or misaligned pointer, max_norm < 0 or NaN; for the
+ * step those of qlora_adamw_step), QL_ERR_UNSUPPORTED (numel >= 2^43),
+ * QL_ERR_WORKSPACE, QL_ERR_CUDA.
+ */
+typedef struct {
+  void* const* data;
+  const int64_t* numel;
+  const int32_t* dt;      /* ql_dtype of each tensor */
+  int64_t count;
+} ql_tensor_list;
+ql_status qlora_grad_norm(const ql_tensor_list* list, float max_norm, float* norm, float* coef, void* ws,
+                          size_t ws_bytes, void* stream);
+ql_status qlora_grad_scale(const ql_tensor_list* list, const float* coef, void* stream);
+ql_status qlora_adamw_step_clipped(float* p, const float* g, float* m, float* v, void* p_bf16, int64_t n, int64_t t,
+                                   float lr, float beta1, float beta2, float eps, float weight_decay,
+                                   const float* coef, void* stream);
+
+/*
+ * The norms before and after a block, fused with the block's gate and the
+ * residual scale, forward and backward.  A decoder block is x' = x + f(norm(x))
+ * around the adapted linears ([P3] "Seeing it in code" adapts every linear of
+ * it); the pages give no formula for the norm, which is the root-mean-square
+ * norm here.  Per token row m of D channels, o = w_offset:
+ *   nh = h rstd_post,  rstd_post = (mean h^2 + eps)^-1/2    (nh = h when w_post is NULL)
+ *   x' = round(alpha x + gate[m / gate_rows] (o + w_post) nh)
+ *   y  = round(x' rstd_pre (o + w_pre)),  rstd_pre = (mean x'^2 + eps)^-1/2
+ * where h is the block's output, x the residual stream and y the next block's
+ * input; x' is rounded to its type before the norm reads it.  All arithmetic
+ * is fp32.  Any of the three parts may be left out, so one call serves the
+ * norm in front of the first block, the one between two blocks and the end.
+ *
+ * ql_block_norm: w_pre, w_post device [D] or NULL; gate device
+ *   [ceil(M / gate_rows), D] or NULL (row m / gate_rows scales token m: gate_rows
+ *   = M for one gate, the sequence length for one per sequence, 1 for one per
+ *   token); all three of type w_dt.  w_offset is added to w_pre and w_post (0, or
+ *   1 for weights stored around zero).
+ * qlora_block_norm_fwd: x device [M, D] of x_dt; h device [M, D] of h_dt, or
+ *   NULL (x' = round(alpha x); w_post and gate are then unused); x_out device
+ *   out [M, D] of x_dt or NULL; y device out [M, D] of y_dt or NULL (no norm;
+ *   w_pre is then unused, and required otherwise).  rstd_pre, rstd_post device
+ *   out fp32 [M] or NULL: what the backward pass needs.  x_out may be x.
+ *   Neither x_out nor y may otherwise overlap another argument.
+ * qlora_block_norm_bwd: gradients of <dx_out, x'> + <dy, y> for the call above:
+ *   x_out device [M, D] of x_dt: x' as stored (only read when dy is given);
+ *   h, rstd_pre, rstd_post as above (rstd_pre when dy is given; rstd_post when h
+ *   and w_post are; h when w_post is given with dh, dw_post or dgate asked for);
+ *   dx_out device [M, D] of x_dt or NULL (zero); dy device [M, D] of dy_dt or
+ *   NULL (zero); at least one of them.
+ *   dx device out [M, D] of x_dt or NULL, may be dx_out; dh device out [M, D] of
+ *   h_dt or NULL; dw_pre, dw_post device out fp32 [D] or NULL (dw_pre needs dy,
+ *   dw_post needs h and w_post); dgate device out fp32 [ceil(M / gate_rows), D]
+ *   or NULL (needs h and the gate).  The sums over tokens are taken in a fixed
+ *   order.  ws >= qlora_workspace_size(QL_OP_BLOCK_NORM_BWD, M, D, gate_rows, 0)
+ *   when dw_pre, dw_post or dgate is asked for (gate_rows 0 without a gate).
+ * M == 0 launches nothing forward and zeroes dw_pre and dw_post backward.
+ * Errors: QL_ERR_INVALID_ARG (M < 0, D < 1, a missing, NULL or misaligned
+ * pointer, gate_rows < 1 with a gate, eps < 0, an unknown dtype),
+ * QL_ERR_UNSUPPORTED (D > QL_MAX_NORM_DIM, M >= 2^31), QL_ERR_WORKSPACE,
+ * QL_ERR_CUDA.
+ */
+#define QL_MAX_NORM_DIM 16384
+typedef struct {
+  const void* w_pre;
+  const void* w_post;
+  const void* gate;
+  ql_dtype w_dt;
+  float w_offset;
+  float alpha;
+  float eps;
+  int64_t gate_rows;
+} ql_block_norm;
+ql_status qlora_block_norm_fwd(const ql_block_norm* norm, const void* x, ql_dtype x_dt, const void* h, ql_dtype h_dt,
+                               int64_t M, int64_t D, void* x_out, void* y, ql_dtype y_dt, float* rstd_pre,
+                               float* rstd_post, void* stream);
+ql_status qlora_block_norm_bwd(const ql_block_norm* norm, const void* x_out, ql_dtype x_dt, const void* h,
+                               ql_dtype h_dt, const float* rstd_pre, const float* rstd_post, const void* dx_out,
+                               const void* dy, ql_dtype dy_dt, int64_t M, int64_t D, void* dx, void* dh,
+                               float* dw_pre, float* dw_post, float* dgate, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * 8-bit integer linear ([P1] "From FP32 to the 4-Bit Horizon" has INT8 between
+ * the 16-bit and the 4-bit formats): both operands int8 with one fp32 scale per
+ * row, so one per token and one per output channel.  This is the 8-bit form of
+ * a merged weight (qlora_merge), not the QLoRA linear's bf16 activations.
+ *
+ * int8_quantize: x device [rows, K] of x_dt -> codes device out int8 [rows, K],
+ *   scales device out fp32 [rows]:  s = fl32(max|x| / 127), code =
+ *   rint(fl32(x / s)) (ties to even) in [-127, 127], 0 where s == 0.  A row with
+ *   a NaN or infinity sets QL_ERR_NONFINITE in the status word; its codes are 0
+ *   and its scale NaN, so that its products are NaN.
+ * int8_gemm: a device int8 [M, K] with a_scales fp32 [M] (tokens), b device int8
+ *   [N, K] with b_scales fp32 [N] (output channels), Y device out [M, N] of y_dt:
+ *     Y[m, n] = round(fl32(fl32(sum_k a[m, k] b[n, k]) fl32(a_scales[m] b_scales[n])))
+ *   The sum is exact (int32); all int8 values are allowed.  M == 0 launches
+ *   nothing.  ws >= qlora_workspace_size(QL_OP_INT8_GEMM, M, N, K, 0) (may be 0;
+ *   ws may then be NULL).
+ * Constraints: K a multiple of 16, K <= QL_MAX_INT8_K; rows, M, N < 2^31 and
+ * ceil(M / 256) ceil(N / 256) < 2^30.  Errors: QL_ERR_INVALID_ARG (rows, N or
+ * K < 1, M < 0, a NULL or misaligned pointer, an unknown dtype),
+ * QL_ERR_UNSUPPORTED (past the constraints), QL_ERR_WORKSPACE, QL_ERR_CUDA.  A
+ * bounded wait that runs out sets QL_ERR_TIMEOUT in the status word.
+ */
+#define QL_MAX_INT8_K 131056
+ql_status int8_quantize(const void* x, ql_dtype x_dt, int64_t rows, int64_t K, int8_t* codes, float* scales,
+                        void* stream);
+ql_status int8_gemm(const int8_t* a, const float* a_scales, const int8_t* b, const float* b_scales, int64_t M,
+                    int64_t N, int64_t K, void* Y, ql_dtype y_dt, void* ws, size_t ws_bytes, void* stream);
+
 /* Workspace query.  op: one of the QL_OP_* values; unused sizes are ignored. */
 #define QL_OP_DOUBLE_QUANT 0   /* M = nb */
 #define QL_OP_FWD 1
 #define QL_OP_BWD 2
 #define QL_OP_NVFP4 3          /* M = n */
+#define QL_OP_BLOCK_NORM_BWD 4 /* M = tokens, N = D, K = gate_rows (0: no gate) */
+#define QL_OP_GRAD_NORM 5      /* M = count */
+#define QL_OP_INT8_GEMM 6
 size_t qlora_workspace_size(int op, int64_t M, int64_t N, int64_t K, int r);
 
 /* Bytes needed for n parameters: ceil(n/2) codes + (dq ? nb + 4*ng + 4 : 4*nb)

@@ -77,3 +77,13 @@ def adamw_step_fp32(p, g, m, v, t: int, lr: float, b1: float = 0.9, b2: float = 
     d = f(f(np.sqrt(f(v / c2))) + eps_)
     p = f(p - f(lr_ * f(f(m / c1) / d)))
     return p, m, v
+
+
+def clip(grads, max_norm):
+    """Global norm of a list of arrays and the coefficient
+    min(1, max_norm / (norm + 1e-6)), in float64."""
+    total = 0.0
+    for g in grads:
+        total += float(np.sum(np.asarray(g, dtype=np.float64) ** 2))
+    norm = np.sqrt(total)
+    return norm, min(1.0, max_norm / (norm + 1e-6))
