@@ -24,7 +24,7 @@ def nvcc() -> str:
 
 def flags() -> list[str]:
     return ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
-            "-Xcompiler", "-fPIC", "-Xcompiler", "-ffp-contract=off", "-shared",
+            "-Xcompiler", "-fPIC", "-Xcompiler", "-ffp-contract=off", "-shared", "-t", "0",
             "-I" + os.path.join(ROOT, "include")]
 
 

@@ -71,6 +71,7 @@ ql_status launch_grad_norm(const ql_tensor_list* list, float max_norm, float* no
                            cudaStream_t st);
 ql_status launch_grad_scale(const ql_tensor_list* list, const float* coef, cudaStream_t st);
 // norm.cu
+unsigned status_word_norm(cudaStream_t st);
 size_t block_norm_bwd_ws(int64_t M, int64_t D, int64_t gate_rows);
 ql_status launch_block_norm_fwd(const ql_block_norm* n, const void* x, ql_dtype x_dt, const void* h, ql_dtype h_dt,
                                 int64_t M, int64_t D, void* x_out, void* y, ql_dtype y_dt, float* rstd_pre,
@@ -585,7 +586,8 @@ ql_status qlora_get_status(void* stream) {
   unsigned v = 0;
   for (unsigned (*word)(cudaStream_t) : {ql::status_word_codec, ql::status_word_gemm, ql::status_word_lora,
                                          ql::status_word_smallm, ql::status_word_diag, ql::status_word_fp4,
-                                         ql::status_word_fp4g, ql::status_word_gradnorm, ql::status_word_int8}) {
+                                         ql::status_word_fp4g, ql::status_word_gradnorm, ql::status_word_int8,
+                                         ql::status_word_norm}) {
     const unsigned w = word(cs);
     if (w == ~0u) return QL_ERR_CUDA;
     v |= w;

@@ -20,9 +20,14 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "sm100.cuh"
 #include "trace.cuh"
 
 namespace ql {
+using namespace sm100;
+
+QL_DEFINE_STATUS_ACCESSOR(status_word_norm)
+
 namespace bn {
 
 constexpr int kMaxD = 16384;      // widest row a block of kMaxThreads holds in registers
@@ -63,8 +68,16 @@ __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(bf16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ float rounded(float v, const float*) { return v; }
-__device__ __forceinline__ float rounded(float v, const bf16*) { return __bfloat162float(__float2bfloat16_rn(v)); }
+// The values as the type stores them (storing them again rounds nothing).
+__device__ __forceinline__ void round8(float (&)[8], float*) {}
+__device__ __forceinline__ void round8(float (&v)[8], bf16*) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const uint32_t p = pack_bf16x2(v[j], v[j + 1]);
+    v[j] = bf16_lo(p);
+    v[j + 1] = bf16_hi(p);
+  }
+}
 
 // Columns c .. c+7 of a row (`row` points at its column 0); columns outside
 // [0, D) read as 0.  `full`: all eight are inside and the address is aligned.
@@ -121,6 +134,59 @@ __device__ __forceinline__ void loadw8(const void* w, bool f32, int64_t base, in
   for (int j = 0; j < 8; ++j) v[j] += off;
 }
 
+// Eight values at a time as four packed pairs (one instruction a pair).
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+// v = v w
+__device__ __forceinline__ void mul8(float (&v)[8], const float (&w)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) mul2(v[j], v[j + 1], v[j], v[j + 1], w[j], w[j + 1]);
+}
+__device__ __forceinline__ void mul8(float (&v)[8], float s) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) mul2(v[j], v[j + 1], v[j], v[j + 1], s, s);
+}
+__device__ __forceinline__ void add8(float (&v)[8], float s) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) add2(v[j], v[j + 1], v[j], v[j + 1], s, s);
+}
+// d = a b + c
+__device__ __forceinline__ void fma8(float (&d)[8], const float (&a)[8], const float (&b)[8], const float (&c)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) fma2(d[j], d[j + 1], a[j], a[j + 1], b[j], b[j + 1], c[j], c[j + 1]);
+}
+__device__ __forceinline__ void fma8(float (&d)[8], float a, const float (&b)[8], const float (&c)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) fma2(d[j], d[j + 1], a, a, b[j], b[j + 1], c[j], c[j + 1]);
+}
+// (s0, s1) += pairwise products
+__device__ __forceinline__ void dot8(float& s0, float& s1, const float (&a)[8], const float (&b)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) fma2(s0, s1, a[j], a[j + 1], b[j], b[j + 1], s0, s1);
+}
+// Columns outside the row (an edge group) to zero.
+__device__ __forceinline__ void mask8(float (&v)[8], int c, int D) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (c + j < 0 || c + j >= D) v[j] = 0.0f;
+}
+
 // Sums of K values over the block (every thread gets them), one barrier: the
 // warps' sums go through buf[K][32], which the caller alternates between two
 // buffers so that a slow warp still reads the previous sums.
@@ -161,9 +227,9 @@ struct FwdArgs {
   const void* w_pre;
   const void* w_post;
   const void* gate;
-  int64_t M, gate_rows;
+  int M, gate_rows;      // both below 2^31: a row's gate takes a 32-bit division
   int D;
-  float alpha, eps, offset;
+  float alpha, eps, offset, inv_d;
   bool w_f32, y_f32;
 };
 
@@ -176,10 +242,10 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxThreads) norm_fwd_kernel(cons
   pdl_trigger();
   const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
   const int nt = WARP ? 32 : blockDim.x;
-  const int64_t m = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+  const int m = WARP ? (int)(blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) : (int)blockIdx.x;
   if (m >= a.M) return;   // WARP only: a whole warp
   const int D = a.D;
-  const int64_t flat = m * D;
+  const int64_t flat = (int64_t)m * D;
   const int shift = GROUPED ? 0 : (int)(flat & 7);
   const XT* x = reinterpret_cast<const XT*>(a.x) + flat;
   const HT* h = reinterpret_cast<const HT*>(a.h) + flat;
@@ -190,7 +256,7 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxThreads) norm_fwd_kernel(cons
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     col[v] = (t + v * nt) * 8 - shift;
-    full[v] = col[v] >= 0 && col[v] + 8 <= D;
+    full[v] = GROUPED || (col[v] >= 0 && col[v] + 8 <= D);
     if (col[v] < D) {
       load8(x, col[v], D, full[v], r[v]);
       if (a.h) load8(h, col[v], D, full[v], hv[v]);
@@ -208,10 +274,10 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxThreads) norm_fwd_kernel(cons
 #pragma unroll
         for (int j = 0; j < 8; ++j) s[0] += hv[v][j] * hv[v][j];
       if (WARP) warp_sums(s); else block_sums(s, red[0]);
-      rs = 1.0f / sqrtf(s[0] / (float)D + a.eps);
+      rs = rsqrtf(s[0] * a.inv_d + a.eps);
       if (t == 0 && a.rstd_post) a.rstd_post[m] = rs;
     }
-    const int64_t grow = a.gate ? (m / a.gate_rows) * D : 0;
+    const int64_t grow = a.gate ? (int64_t)(m / a.gate_rows) * D : 0;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       if (col[v] >= D) continue;
@@ -232,16 +298,15 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxThreads) norm_fwd_kernel(cons
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const bool in = col[v] < D;
+    round8(r[v], (XT*)nullptr);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      r[v][j] = rounded(r[v][j], (const XT*)nullptr);
-      if (in && (GROUPED || full[v] || (col[v] + j >= 0 && col[v] + j < D))) s[0] += r[v][j] * r[v][j];
-    }
+    for (int j = 0; j < 8; ++j)
+      if (in && (full[v] || (col[v] + j >= 0 && col[v] + j < D))) s[0] += r[v][j] * r[v][j];
     if (in && a.x_out) store8(reinterpret_cast<XT*>(a.x_out) + flat, col[v], D, full[v], r[v]);
   }
   if (!a.y) return;
   if (WARP) warp_sums(s); else block_sums(s, red[1]);
-  const float rs = 1.0f / sqrtf(s[0] / (float)D + a.eps);
+  const float rs = rsqrtf(s[0] * a.inv_d + a.eps);
   if (t == 0 && a.rstd_pre) a.rstd_pre[m] = rs;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
@@ -254,6 +319,160 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxThreads) norm_fwd_kernel(cons
       store8(reinterpret_cast<float*>(a.y) + flat, col[v], D, full[v], wv);
     else
       store8(reinterpret_cast<bf16*>(a.y) + flat, col[v], D, full[v], wv);
+  }
+}
+
+// The same for many rows.  Each block walks over rows blockIdx.x, blockIdx.x +
+// gridDim.x, ...; their x and h arrive by bulk copies in a ring of `stages`
+// rows in shared memory, so the next rows are on their way while this one waits
+// for its two sums.  Two groups per thread; 64 registers, so 1024 threads an SM
+// are at work.  The product gate (o + w_post) stays in registers while the gate's
+// row does not change; w_pre comes from L1.
+constexpr int kStreamVpt = 2;
+constexpr int kStreamThreads = 1024;
+constexpr int kMaxStages = 4;
+
+template <typename XT, typename HT>
+__host__ __device__ constexpr int stream_x_bytes(int groups) { return groups * 8 * (int)sizeof(XT); }
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+template <typename XT, typename HT, typename WT, bool GROUPED>
+__global__ void __launch_bounds__(kStreamThreads) norm_fwd_stream_kernel(const FwdArgs a, int stages, int groups) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float red[3][32];
+  __shared__ uint64_t full_bar[kMaxStages];
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
+  constexpr int VPT = kStreamVpt;
+  const int t = threadIdx.x, nt = blockDim.x, D = a.D;
+  const int x_bytes = groups * 8 * (int)sizeof(XT), stage_bytes = groups * 8 * (int)(sizeof(XT) + sizeof(HT));
+  if (t == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&full_bar[s], 1);
+    abort_word = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  const int64_t total = (int64_t)a.M * D;
+  // The groups that row m touches, as far as they lie inside the tensor: the
+  // one group that a last row may share with what is behind the tensor is read
+  // from global memory, value by value.
+  auto issue = [&](int64_t m, int s) {
+    const int64_t g0 = m * D / 8, g1 = GROUPED ? (m + 1) * D / 8 : min(((m + 1) * D + 7) / 8, total / 8);
+    uint8_t* st = ring + (size_t)s * stage_bytes;
+    const uint32_t n = (uint32_t)(g1 - g0) * 8;
+    mbar_arrive_expect_tx(&full_bar[s], n * (uint32_t)(sizeof(XT) + sizeof(HT)));
+    if (n) {
+      bulk_load(st, reinterpret_cast<const XT*>(a.x) + g0 * 8, n * (uint32_t)sizeof(XT), &full_bar[s]);
+      bulk_load(st + x_bytes, reinterpret_cast<const HT*>(a.h) + g0 * 8, n * (uint32_t)sizeof(HT), &full_bar[s]);
+    }
+  };
+  if (t == 0)
+    for (int s = 0; s < stages; ++s)
+      if (blockIdx.x + (int64_t)s * gridDim.x < a.M) issue(blockIdx.x + (int64_t)s * gridDim.x, s);
+
+  float gw[VPT][8];
+  int held = -1;          // the gate row in gw
+  int s = 0, use = 0, parity = 0;
+  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+    const int64_t flat = m * D;
+    const int shift = GROUPED ? 0 : (int)(flat & 7);
+    const int grow = a.gate ? (int)m / a.gate_rows : 0;
+    const bool fresh = !GROUPED || grow != held;
+    held = grow;
+    const XT* xs = reinterpret_cast<const XT*>(ring + (size_t)s * stage_bytes);
+    const HT* hs = reinterpret_cast<const HT*>(ring + (size_t)s * stage_bytes + x_bytes);
+    mbar_wait(&full_bar[s], use & 1, abort_flag, 1u << 22);
+    float v[VPT][8];
+    float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int g = t + k * nt, c = g * 8 - shift;
+      if (c >= D) continue;
+      if (GROUPED || flat + c + 8 <= total) {
+        Raw8<HT> raw;
+        raw.load(hs + g * 8);
+        raw.to_f32(v[k]);
+      } else {
+        load8(reinterpret_cast<const HT*>(a.h) + flat, c, D, false, v[k]);
+      }
+      if (!GROUPED) mask8(v[k], c, D);
+      dot8(s0, s1, v[k], v[k]);
+      if (fresh) {
+        float w[8];
+        loadw8(a.w_post, sizeof(WT) == 4, 0, c, D, GROUPED, a.w_post ? a.offset : 1.0f, w);
+        loadw8(a.gate, sizeof(WT) == 4, (int64_t)grow * D, c, D, GROUPED, a.gate ? 0.0f : 1.0f, gw[k]);
+        mul8(gw[k], w);
+      }
+    }
+    float rs = 1.0f;
+    if (a.w_post) {
+      float sum[1] = {s0 + s1};
+      block_sums(sum, red[2]);
+      rs = rsqrtf(sum[0] * a.inv_d + a.eps);
+      if (t == 0 && a.rstd_post) a.rstd_post[m] = rs;
+    }
+    s0 = s1 = 0.0f;
+    Raw8<WT> pre[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int g = t + k * nt, c = g * 8 - shift;
+      if (c >= D) continue;
+      float xv[8];
+      if (GROUPED || flat + c + 8 <= total) {
+        Raw8<XT> raw;
+        raw.load(xs + g * 8);
+        raw.to_f32(xv);
+      } else {
+        load8(reinterpret_cast<const XT*>(a.x) + flat, c, D, false, xv);
+      }
+      mul8(v[k], rs);
+      mul8(v[k], gw[k]);
+      fma8(v[k], a.alpha, xv, v[k]);
+      if (!GROUPED) mask8(v[k], c, D);
+      round8(v[k], (XT*)nullptr);
+      dot8(s0, s1, v[k], v[k]);
+      if (a.x_out) store8(reinterpret_cast<XT*>(a.x_out) + flat, c, D, GROUPED || (c >= 0 && c + 8 <= D), v[k]);
+      if (GROUPED && a.y) pre[k].load(reinterpret_cast<const WT*>(a.w_pre) + c);   // ahead of the barrier
+    }
+    float sum[1] = {s0 + s1};
+    block_sums(sum, red[parity]);   // also: every thread has read the stage
+    parity ^= 1;
+    if (t == 0 && m + (int64_t)stages * gridDim.x < a.M) issue(m + (int64_t)stages * gridDim.x, s);
+    if (++s == stages) {
+      s = 0;
+      ++use;
+    }
+    if (a.y) {
+      const float rx = rsqrtf(sum[0] * a.inv_d + a.eps);
+      if (t == 0 && a.rstd_pre) a.rstd_pre[m] = rx;
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int c = (t + k * nt) * 8 - shift;
+        if (c >= D) continue;
+        float w[8];
+        if (GROUPED) {
+          pre[k].to_f32(w);
+          add8(w, a.offset);
+        } else {
+          loadw8(a.w_pre, sizeof(WT) == 4, 0, c, D, false, a.offset, w);
+        }
+        mul8(v[k], rx);
+        mul8(v[k], w);
+        const bool full = GROUPED || (c >= 0 && c + 8 <= D);
+        if (a.y_f32)
+          store8(reinterpret_cast<float*>(a.y) + flat, c, D, full, v[k]);
+        else
+          store8(reinterpret_cast<bf16*>(a.y) + flat, c, D, full, v[k]);
+      }
+    }
   }
 }
 
@@ -291,7 +510,7 @@ struct BwdArgs {
   float* part_s;        // [chunks][D], or NULL
   int64_t M;
   int D;
-  float alpha, offset;
+  float alpha, offset, inv_d;
   bool w_f32, post, load_h;
   BwdPlan plan;
 };
@@ -357,7 +576,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const BwdArgs a) 
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
         const int c = (t + v * nt) * 8 - shift;
-        const bool full = c >= 0 && c + 8 <= D;
+        const bool full = GROUPED || (c >= 0 && c + 8 <= D);
         if (c >= D) continue;
         float dy[8];
         if (a.dy) {
@@ -414,12 +633,12 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const BwdArgs a) 
       // dr = u - rsx c1 n with c1 = mean(dn n), so mean(dnh nh) = mean(u q) - rsx c1 mean(n q)
       block_sums(s, red[parity]);
       parity ^= 1;
-      const float k1 = rsx * (s[0] / (float)D);
-      const float c2 = (s[1] - k1 * s[2]) / (float)D;
+      const float k1 = rsx * (s[0] * a.inv_d);
+      const float c2 = (s[1] - k1 * s[2]) * a.inv_d;
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
         const int c = (t + v * nt) * 8 - shift;
-        const bool full = c >= 0 && c + 8 <= D;
+        const bool full = GROUPED || (c >= 0 && c + 8 <= D);
         if (c >= D) continue;
         float o[8], sv[8];
 #pragma unroll
@@ -572,8 +791,39 @@ ql_status run_fwd(const FwdArgs& a, cudaStream_t st) {
   return QL_OK;
 }
 
+template <typename XT, typename HT, typename WT, bool GROUPED>
+ql_status run_stream(const FwdArgs& a, cudaStream_t st) {
+  const auto kernel = norm_fwd_stream_kernel<XT, HT, WT, GROUPED>;
+  constexpr int kMost = 200 * 1024;
+  if (per_device(reinterpret_cast<const void*>(kernel), 0, [kernel] {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess) {
+          cudaGetLastError();
+          return -1;
+        }
+        return 1;
+      }) < 0)
+    return QL_ERR_CUDA;
+  const int groups = row_groups(a.D);
+  const unsigned threads = row_threads(a.D, kStreamVpt);
+  const int stage = groups * 8 * (int)(sizeof(XT) + sizeof(HT));
+  // as many blocks as 1024 threads an SM allow, if two rows each fit; then as many rows as fit
+  int per_sm = std::max(1, kStreamThreads / (int)threads);
+  while (per_sm > 1 && per_sm * (2 * stage + 2048) > kMost) --per_sm;
+  const int stages = std::max(1, std::min(kMaxStages, (kMost / per_sm - 2048) / stage));
+  const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
+  const int64_t grid = std::min<int64_t>(a.M, (int64_t)sms * per_sm);
+  TraceScope ts(TK_NORM, st);
+  QL_CUDA_TRY(launch(kernel, dim3((unsigned)grid), dim3(threads), (size_t)stages * stage, st, 1, 1, a, stages, groups));
+  QL_LAUNCH_CHECK();
+  return QL_OK;
+}
+
 template <typename XT, typename HT, bool GROUPED>
 ql_status pick_fwd(const FwdArgs& a, cudaStream_t st) {
+  const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
+  const int groups = row_groups(a.D);
+  if (a.h && groups > 128 && groups <= kStreamVpt * kStreamThreads && a.M > 4 * sms)
+    return a.w_f32 ? run_stream<XT, HT, float, GROUPED>(a, st) : run_stream<XT, HT, bf16, GROUPED>(a, st);
   // rows of up to 128 groups: one warp each, no block barrier
   if (row_groups(a.D) <= 128) return run_fwd<XT, HT, 4, GROUPED, true>(a, st);
   switch (groups_per_thread(a.D)) {
@@ -644,11 +894,12 @@ ql_status launch_block_norm_fwd(const ql_block_norm* n, const void* x, ql_dtype 
   a.w_pre = n->w_pre;
   a.w_post = n->w_post;
   a.gate = n->gate;
-  a.M = M;
-  a.gate_rows = n->gate_rows;
+  a.M = (int)M;
+  a.gate_rows = (int)std::min<int64_t>(n->gate_rows, M);
   a.D = (int)D;
   a.alpha = n->alpha;
   a.eps = n->eps;
+  a.inv_d = 1.0f / (float)D;
   a.offset = n->w_offset;
   a.w_f32 = n->w_dt == QL_F32;
   a.y_f32 = y_dt == QL_F32;
@@ -688,6 +939,7 @@ ql_status launch_block_norm_bwd(const ql_block_norm* n, const void* x_out, ql_dt
   a.M = M;
   a.D = (int)D;
   a.alpha = n->alpha;
+  a.inv_d = 1.0f / (float)D;
   a.offset = n->w_offset;
   a.w_f32 = n->w_dt == QL_F32;
   a.post = h && n->w_post;
