@@ -116,22 +116,52 @@ __device__ __forceinline__ void store8(T* row, int c, int D, bool full, const fl
   }
 }
 
-// A weight or gate row of either type: values off + w[c .. c+7] (off alone, or
-// `off` for a NULL w; 0 outside the row).  The row itself starts on 16 bytes
-// only where D is a multiple of 8 (`vec`).
-__device__ __forceinline__ void loadw8(const void* w, bool f32, int64_t base, int c, int D, bool vec, float off,
-                                       float (&v)[8]) {
-  if (!w) {
+// Columns c .. c+7 of the row of D values that starts at index `base` of an array
+// of `len` values, for a D that is no multiple of 8, where the row starts
+// anywhere in a group: two aligned groups, shifted by the values that the first
+// one has too many (the same number for all threads of a row).  Groups that
+// reach outside the array or the row are read value by value (0 outside the row).
+__device__ __forceinline__ void shifted8(const bf16* w, int64_t base, int64_t len, int c, int D, float (&v)[8]) {
+  const int64_t i = base + c;
+  if (c >= 0 && c + 8 <= D && (i >> 3) * 8 + 16 <= len) {
+    const uint4* p = reinterpret_cast<const uint4*>(w) + (i >> 3);
+    const uint4 a = p[0], b = p[1];
+    const int sh = (int)(i & 7);
+    uint32_t q[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = off;
-    return;
+    for (int k = 0; k < 6; ++k) q[k] = sh & 4 ? q[k + 2] : q[k];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) q[k] = sh & 2 ? q[k + 1] : q[k];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t r = sh & 1 ? __funnelshift_r(q[k], q[k + 1], 16) : q[k];
+      v[2 * k] = bf16_lo(r);
+      v[2 * k + 1] = bf16_hi(r);
+    }
+  } else {
+    load8(w + base, c, D, false, v);
   }
-  if (f32)
-    load8(reinterpret_cast<const float*>(w) + base, c, D, vec, v);
-  else
-    load8(reinterpret_cast<const bf16*>(w) + base, c, D, vec, v);
+}
+__device__ __forceinline__ void shifted8(const float* w, int64_t base, int64_t len, int c, int D, float (&v)[8]) {
+  const int64_t i = base + c;
+  if (c >= 0 && c + 8 <= D && (i >> 3) * 8 + 16 <= len) {
+    const float4* p = reinterpret_cast<const float4*>(w) + (i >> 3) * 2;
+    float q[16];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] += off;
+    for (int k = 0; k < 4; ++k) {
+      const float4 f = p[k];
+      q[4 * k] = f.x; q[4 * k + 1] = f.y; q[4 * k + 2] = f.z; q[4 * k + 3] = f.w;
+    }
+    const int sh = (int)(i & 7);
+#pragma unroll
+    for (int k = 0; k < 12; ++k) q[k] = sh & 4 ? q[k + 4] : q[k];
+#pragma unroll
+    for (int k = 0; k < 10; ++k) q[k] = sh & 2 ? q[k + 2] : q[k];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = sh & 1 ? q[k + 1] : q[k];
+  } else {
+    load8(w + base, c, D, false, v);
+  }
 }
 
 // Eight values at a time as four packed pairs (one instruction a pair).
@@ -187,6 +217,29 @@ __device__ __forceinline__ void mask8(float (&v)[8], int c, int D) {
     if (c + j < 0 || c + j >= D) v[j] = 0.0f;
 }
 
+// A weight or gate row of either type: off + w[base + c .. base + c + 7] (`off`
+// alone for a NULL w); `len` values in all.
+template <bool GROUPED>
+__device__ __forceinline__ void loadw8(const void* w, bool f32, int64_t base, int64_t len, int c, int D, float off,
+                                       float (&v)[8]) {
+  if (!w) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = off;
+    return;
+  }
+  if (GROUPED) {
+    if (f32)
+      load8(reinterpret_cast<const float*>(w) + base, c, D, true, v);
+    else
+      load8(reinterpret_cast<const bf16*>(w) + base, c, D, true, v);
+  } else if (f32) {
+    shifted8(reinterpret_cast<const float*>(w), base, len, c, D, v);
+  } else {
+    shifted8(reinterpret_cast<const bf16*>(w), base, len, c, D, v);
+  }
+  add8(v, off);
+}
+
 // Sums of K values over the block (every thread gets them), one barrier: the
 // warps' sums go through buf[K][32], which the caller alternates between two
 // buffers so that a slow warp still reads the previous sums.
@@ -227,6 +280,7 @@ struct FwdArgs {
   const void* w_pre;
   const void* w_post;
   const void* gate;
+  int64_t gate_len;      // values of the gate
   int M, gate_rows;      // both below 2^31: a row's gate takes a 32-bit division
   int D;
   float alpha, eps, offset, inv_d;
@@ -282,8 +336,8 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxThreads) norm_fwd_kernel(cons
     for (int v = 0; v < VPT; ++v) {
       if (col[v] >= D) continue;
       float wv[8], gv[8];
-      loadw8(a.w_post, a.w_f32, 0, col[v], D, GROUPED, a.w_post ? a.offset : 1.0f, wv);
-      loadw8(a.gate, a.w_f32, grow, col[v], D, GROUPED, a.gate ? 0.0f : 1.0f, gv);
+      loadw8<GROUPED>(a.w_post, a.w_f32, 0, D, col[v], D, a.w_post ? a.offset : 1.0f, wv);
+      loadw8<GROUPED>(a.gate, a.w_f32, grow, a.gate_len, col[v], D, a.gate ? 0.0f : 1.0f, gv);
 #pragma unroll
       for (int j = 0; j < 8; ++j) r[v][j] = a.alpha * r[v][j] + gv[j] * (hv[v][j] * rs * wv[j]);
     }
@@ -312,7 +366,7 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxThreads) norm_fwd_kernel(cons
   for (int v = 0; v < VPT; ++v) {
     if (col[v] >= D) continue;
     float wv[8];
-    loadw8(a.w_pre, a.w_f32, 0, col[v], D, GROUPED, a.offset, wv);
+    loadw8<GROUPED>(a.w_pre, a.w_f32, 0, D, col[v], D, a.offset, wv);
 #pragma unroll
     for (int j = 0; j < 8; ++j) wv[j] *= r[v][j] * rs;
     if (a.y_f32)
@@ -379,14 +433,15 @@ __global__ void __launch_bounds__(kStreamThreads) norm_fwd_stream_kernel(const F
       if (blockIdx.x + (int64_t)s * gridDim.x < a.M) issue(blockIdx.x + (int64_t)s * gridDim.x, s);
 
   float gw[VPT][8];
-  int held = -1;          // the gate row in gw
+  int held = -1, held_shift = 0;   // the gate row in gw, and where its groups start
   int s = 0, use = 0, parity = 0;
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
     const int64_t flat = m * D;
     const int shift = GROUPED ? 0 : (int)(flat & 7);
     const int grow = a.gate ? (int)m / a.gate_rows : 0;
-    const bool fresh = !GROUPED || grow != held;
+    const bool fresh = grow != held || shift != held_shift;
     held = grow;
+    held_shift = shift;
     const XT* xs = reinterpret_cast<const XT*>(ring + (size_t)s * stage_bytes);
     const HT* hs = reinterpret_cast<const HT*>(ring + (size_t)s * stage_bytes + x_bytes);
     mbar_wait(&full_bar[s], use & 1, abort_flag, 1u << 22);
@@ -403,12 +458,12 @@ __global__ void __launch_bounds__(kStreamThreads) norm_fwd_stream_kernel(const F
       } else {
         load8(reinterpret_cast<const HT*>(a.h) + flat, c, D, false, v[k]);
       }
-      if (!GROUPED) mask8(v[k], c, D);
+      if (!GROUPED && (c < 0 || c + 8 > D)) mask8(v[k], c, D);
       dot8(s0, s1, v[k], v[k]);
       if (fresh) {
         float w[8];
-        loadw8(a.w_post, sizeof(WT) == 4, 0, c, D, GROUPED, a.w_post ? a.offset : 1.0f, w);
-        loadw8(a.gate, sizeof(WT) == 4, (int64_t)grow * D, c, D, GROUPED, a.gate ? 0.0f : 1.0f, gw[k]);
+        loadw8<GROUPED>(a.w_post, sizeof(WT) == 4, 0, D, c, D, a.w_post ? a.offset : 1.0f, w);
+        loadw8<GROUPED>(a.gate, sizeof(WT) == 4, (int64_t)grow * D, a.gate_len, c, D, a.gate ? 0.0f : 1.0f, gw[k]);
         mul8(gw[k], w);
       }
     }
@@ -436,7 +491,7 @@ __global__ void __launch_bounds__(kStreamThreads) norm_fwd_stream_kernel(const F
       mul8(v[k], rs);
       mul8(v[k], gw[k]);
       fma8(v[k], a.alpha, xv, v[k]);
-      if (!GROUPED) mask8(v[k], c, D);
+      if (!GROUPED && (c < 0 || c + 8 > D)) mask8(v[k], c, D);
       round8(v[k], (XT*)nullptr);
       dot8(s0, s1, v[k], v[k]);
       if (a.x_out) store8(reinterpret_cast<XT*>(a.x_out) + flat, c, D, GROUPED || (c >= 0 && c + 8 <= D), v[k]);
@@ -462,7 +517,7 @@ __global__ void __launch_bounds__(kStreamThreads) norm_fwd_stream_kernel(const F
           pre[k].to_f32(w);
           add8(w, a.offset);
         } else {
-          loadw8(a.w_pre, sizeof(WT) == 4, 0, c, D, false, a.offset, w);
+          loadw8<GROUPED>(a.w_pre, sizeof(WT) == 4, 0, D, c, D, a.offset, w);
         }
         mul8(v[k], rx);
         mul8(v[k], w);
@@ -504,6 +559,7 @@ struct BwdArgs {
   const void* w_pre;
   const void* w_post;
   const void* gate;
+  int64_t gate_len;     // values of the gate
   float* dgate;         // written here when a gate's rows are one chunk
   float* part_pre;      // [blocks][D], or NULL
   float* part_post;     // [blocks][D], or NULL
@@ -595,8 +651,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const BwdArgs a) 
         }
         float w[8];
         if (a.dh) {
-          loadw8(a.w_post, a.w_f32, 0, c, D, GROUPED, a.w_post ? a.offset : 1.0f, w);
-          loadw8(a.gate, a.w_f32, grow, c, D, GROUPED, a.gate ? 0.0f : 1.0f, gw[v]);
+          loadw8<GROUPED>(a.w_post, a.w_f32, 0, D, c, D, a.w_post ? a.offset : 1.0f, w);
+          loadw8<GROUPED>(a.gate, a.w_f32, grow, a.gate_len, c, D, a.gate ? 0.0f : 1.0f, gw[v]);
 #pragma unroll
           for (int j = 0; j < 8; ++j) gw[v][j] *= w[j];
         } else {
@@ -606,7 +662,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const BwdArgs a) 
 #pragma unroll
         for (int j = 0; j < 8; ++j) nh[v][j] *= rsh;
         if (a.dy) {
-          loadw8(a.w_pre, a.w_f32, 0, c, D, GROUPED, a.offset, w);
+          loadw8<GROUPED>(a.w_pre, a.w_f32, 0, D, c, D, a.offset, w);
           float dyn[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -811,7 +867,8 @@ ql_status run_stream(const FwdArgs& a, cudaStream_t st) {
   while (per_sm > 1 && per_sm * (2 * stage + 2048) > kMost) --per_sm;
   const int stages = std::max(1, std::min(kMaxStages, (kMost / per_sm - 2048) / stage));
   const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
-  const int64_t grid = std::min<int64_t>(a.M, (int64_t)sms * per_sm);
+  // a multiple of 8 blocks: 8 rows on, a row starts at the same place of a group
+  const int64_t grid = std::min<int64_t>(a.M, (int64_t)sms * per_sm / 8 * 8);
   TraceScope ts(TK_NORM, st);
   QL_CUDA_TRY(launch(kernel, dim3((unsigned)grid), dim3(threads), (size_t)stages * stage, st, 1, 1, a, stages, groups));
   QL_LAUNCH_CHECK();
@@ -822,7 +879,7 @@ template <typename XT, typename HT, bool GROUPED>
 ql_status pick_fwd(const FwdArgs& a, cudaStream_t st) {
   const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
   const int groups = row_groups(a.D);
-  if (a.h && groups > 128 && groups <= kStreamVpt * kStreamThreads && a.M > 4 * sms)
+  if (a.h && groups > 128 && groups <= kStreamVpt * kStreamThreads && a.M > sms)
     return a.w_f32 ? run_stream<XT, HT, float, GROUPED>(a, st) : run_stream<XT, HT, bf16, GROUPED>(a, st);
   // rows of up to 128 groups: one warp each, no block barrier
   if (row_groups(a.D) <= 128) return run_fwd<XT, HT, 4, GROUPED, true>(a, st);
@@ -896,6 +953,7 @@ ql_status launch_block_norm_fwd(const ql_block_norm* n, const void* x, ql_dtype 
   a.gate = n->gate;
   a.M = (int)M;
   a.gate_rows = (int)std::min<int64_t>(n->gate_rows, M);
+  a.gate_len = n->gate ? (M + n->gate_rows - 1) / n->gate_rows * D : 0;
   a.D = (int)D;
   a.alpha = n->alpha;
   a.eps = n->eps;
@@ -935,6 +993,7 @@ ql_status launch_block_norm_bwd(const ql_block_norm* n, const void* x_out, ql_dt
   a.w_pre = n->w_pre;
   a.w_post = n->w_post;
   a.gate = n->gate;
+  a.gate_len = n->gate ? a.plan.groups * D : 0;
   a.dgate = dgate;
   a.M = M;
   a.D = (int)D;
