@@ -128,8 +128,14 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# The current stream's handle without building a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
@@ -307,30 +313,40 @@ def qlora_silu_gate_bwd(dh, g, u, dg, du, stream=None) -> None:
 # The calls below take their sizes from the tensors, so they check that every
 # tensor is contiguous, of a known type, on the current device and as large as
 # the others make it: the library sees pointers only.
-def _buf(t, name: str, shape, dtypes=None) -> int | None:
-    """The address of a tensor of this shape, or None for None."""
+def _buf(t, name: str, shape, dev: int, dtype=None):
+    """The address of a tensor of this shape (and type) on device `dev`, or None for None."""
     if t is None:
         return None
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} instead of {tuple(shape)}")
-    if dtypes is not None and t.dtype not in dtypes:
-        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype} instead of {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
     return t.data_ptr()
 
 
-_F32 = (torch.float32,)
-_F32_BF16 = (torch.float32, torch.bfloat16)
-_I8 = (torch.int8,)
+_DT = {torch.float32: QL_F32, torch.bfloat16: QL_BF16}
+_F32, _I8 = torch.float32, torch.int8
+_device = torch.cuda.current_device
 
 
-def _ws(ws) -> tuple[int | None, int]:
+def _dt_of(t) -> int:
+    """The library's type of a tensor, 0 for None."""
+    if t is None:
+        return 0
+    try:
+        return _DT[t.dtype]
+    except KeyError:
+        raise TypeError(f"unsupported dtype {t.dtype}") from None
+
+
+def _ws(ws, dev: int):
     if ws is None:
         return None, 0
-    return _buf(ws, "ws", ws.shape), ws.numel() * ws.element_size()
+    return _buf(ws, "ws", ws.shape, dev), ws.nbytes
 
 
 class TensorList:
@@ -353,35 +369,38 @@ class TensorList:
         self._desc = ql_tensor_list(ctypes.cast(self._data, ctypes.POINTER(ctypes.c_void_p)),
                                     ctypes.cast(self._numel, ctypes.POINTER(ctypes.c_int64)),
                                     ctypes.cast(self._dt, ctypes.POINTER(ctypes.c_int32)), n)
+        self._ref = ctypes.byref(self._desc)
 
     def __len__(self) -> int:
         return len(self.tensors)
 
-    def desc(self) -> ql_tensor_list:
-        if self.device is not None and self.device != torch.cuda.current_device():
+    def desc(self, dev: int):
+        if self.device is not None and self.device != dev:
             raise ValueError(f"the list is on cuda:{self.device}, not on the current CUDA device")
-        return self._desc
+        return self._ref
 
 
 def qlora_grad_norm(tensors: TensorList, max_norm: float, norm, coef, ws, stream=None) -> None:
     """norm = sqrt(sum of squares over all tensors), coef = min(1, max_norm / (norm + 1e-6)); fp32 [1] outputs or None."""
-    wp, wb = _ws(ws)
-    _check(LIB.qlora_grad_norm(ctypes.byref(tensors.desc()), float(max_norm), _buf(norm, "norm", (1,), _F32),
-                               _buf(coef, "coef", (1,), _F32), wp, wb, _stream(stream)), "qlora_grad_norm")
+    dev = _device()
+    wp, wb = _ws(ws, dev)
+    _check(LIB.qlora_grad_norm(tensors.desc(dev), max_norm, _buf(norm, "norm", (1,), dev, _F32),
+                               _buf(coef, "coef", (1,), dev, _F32), wp, wb, _stream(stream)), "qlora_grad_norm")
 
 
 def qlora_grad_scale(tensors: TensorList, coef, stream=None) -> None:
     """Every value of every tensor times coef [1] (a device value), in place."""
-    _check(LIB.qlora_grad_scale(ctypes.byref(tensors.desc()), _buf(coef, "coef", (1,), _F32), _stream(stream)),
+    dev = _device()
+    _check(LIB.qlora_grad_scale(tensors.desc(dev), _buf(coef, "coef", (1,), dev, _F32), _stream(stream)),
            "qlora_grad_scale")
 
 
 def qlora_adamw_step_clipped(p, g, m, v, n: int, t: int, lr: float, coef, beta1: float = 0.9, beta2: float = 0.999,
                              eps: float = 1e-8, weight_decay: float = 0.0, p_bf16=None, stream=None) -> None:
     """qlora_adamw_step on g times coef [1] (a device value, from qlora_grad_norm); g is only read."""
-    _check(LIB.qlora_adamw_step_clipped(_ptr(p), _ptr(g), _ptr(m), _ptr(v), _ptr(p_bf16), int(n), int(t), float(lr),
-                                        float(beta1), float(beta2), float(eps), float(weight_decay),
-                                        _buf(coef, "coef", (1,), _F32), _stream(stream)), "qlora_adamw_step_clipped")
+    _check(LIB.qlora_adamw_step_clipped(_ptr(p), _ptr(g), _ptr(m), _ptr(v), _ptr(p_bf16), n, t, lr, beta1, beta2, eps,
+                                        weight_decay, _buf(coef, "coef", (1,), _device(), _F32), _stream(stream)),
+           "qlora_adamw_step_clipped")
 
 
 class BlockNorm:
@@ -398,26 +417,22 @@ class BlockNorm:
         if gate is not None and (gate.dim() != 2 or self.gate_rows < 1):
             raise ValueError("gate must be [gates, D] with gate_rows >= 1")
         self._w_dt = _dt(given[0].dtype) if given else QL_F32
-        self._checked = None
 
-    def desc(self, M: int, D: int) -> ql_block_norm:
-        key = (M, D, torch.cuda.current_device())
-        if self._checked is None or self._checked[0] != key:
-            G = -(-M // self.gate_rows) if self.gate is not None else 0
-            self._checked = (key, ql_block_norm(_buf(self.w_pre, "w_pre", (D,)), _buf(self.w_post, "w_post", (D,)),
-                                                _buf(self.gate, "gate", (G, D)), self._w_dt, self.w_offset,
-                                                self.alpha, self.eps, self.gate_rows))
-        return self._checked[1]
+    def desc(self, M: int, D: int, dev: int):
+        G = -(-M // self.gate_rows) if self.gate is not None else 0
+        return ctypes.byref(ql_block_norm(_buf(self.w_pre, "w_pre", (D,), dev), _buf(self.w_post, "w_post", (D,), dev),
+                                          _buf(self.gate, "gate", (G, D), dev), self._w_dt, self.w_offset, self.alpha,
+                                          self.eps, self.gate_rows))
 
 
 def qlora_block_norm_fwd(norm: BlockNorm, x, h, x_out, y, rstd_pre=None, rstd_post=None, stream=None) -> None:
     """x_out = alpha x + gate * post_norm(h), y = pre_norm(x_out); h, x_out or y, and the saved rstd [M], may be None."""
     M, D = shape = x.shape
-    d = norm.desc(M, D)
+    dev, rows = _device(), (M,)
     _check(LIB.qlora_block_norm_fwd(
-        ctypes.byref(d), _buf(x, "x", shape), _dt(x.dtype), _buf(h, "h", shape), 0 if h is None else _dt(h.dtype), M, D,
-        _buf(x_out, "x_out", shape, (x.dtype,)), _buf(y, "y", shape), 0 if y is None else _dt(y.dtype),
-        _buf(rstd_pre, "rstd_pre", (M,), _F32), _buf(rstd_post, "rstd_post", (M,), _F32), _stream(stream)),
+        norm.desc(M, D, dev), _buf(x, "x", shape, dev), _dt_of(x), _buf(h, "h", shape, dev), _dt_of(h), M, D,
+        _buf(x_out, "x_out", shape, dev, x.dtype), _buf(y, "y", shape, dev), _dt_of(y),
+        _buf(rstd_pre, "rstd_pre", rows, dev, _F32), _buf(rstd_post, "rstd_post", rows, dev, _F32), _stream(stream)),
         "qlora_block_norm_fwd")
 
 
@@ -425,38 +440,39 @@ def qlora_block_norm_bwd(norm: BlockNorm, x_out, h, rstd_pre, rstd_post, dx_out,
                          dgate=None, ws=None, stream=None) -> None:
     """Gradients of qlora_block_norm_fwd: dx [M, D] and dh [M, D] from dx_out and dy (either may be None), and the
     fp32 sums dw_pre [D], dw_post [D] and dgate [G, D] where given (they need the workspace)."""
-    given = dy if dy is not None else dx_out
-    M, D = shape = given.shape
-    d = norm.desc(M, D)
-    stream_t = next((t for t in (x_out, dx_out, dx) if t is not None), None)
-    xt = stream_t.dtype if stream_t is not None else torch.float32
-    block_t = h if h is not None else dh
-    ht = block_t.dtype if block_t is not None else xt
-    G = d.gate_rows and -(-M // d.gate_rows)
-    wp, wb = _ws(ws)
+    M, D = shape = (dy if dy is not None else dx_out).shape
+    dev, rows = _device(), (M,)
+    xs = x_out if x_out is not None else dx_out if dx_out is not None else dx
+    xt = torch.float32 if xs is None else xs.dtype
+    hs = h if h is not None else dh
+    ht = xt if hs is None else hs.dtype
+    G = -(-M // norm.gate_rows) if norm.gate is not None else 0
+    wp, wb = _ws(ws, dev)
     _check(LIB.qlora_block_norm_bwd(
-        ctypes.byref(d), _buf(x_out, "x_out", shape, (xt,)), _dt(xt), _buf(h, "h", shape, (ht,)), _dt(ht),
-        _buf(rstd_pre, "rstd_pre", (M,), _F32), _buf(rstd_post, "rstd_post", (M,), _F32),
-        _buf(dx_out, "dx_out", shape, (xt,)), _buf(dy, "dy", shape), 0 if dy is None else _dt(dy.dtype), M, D,
-        _buf(dx, "dx", shape, (xt,)), _buf(dh, "dh", shape, (ht,)), _buf(dw_pre, "dw_pre", (D,), _F32),
-        _buf(dw_post, "dw_post", (D,), _F32), _buf(dgate, "dgate", (G, D), _F32), wp, wb, _stream(stream)),
+        norm.desc(M, D, dev), _buf(x_out, "x_out", shape, dev, xt), _dt(xt), _buf(h, "h", shape, dev, ht), _dt(ht),
+        _buf(rstd_pre, "rstd_pre", rows, dev, _F32), _buf(rstd_post, "rstd_post", rows, dev, _F32),
+        _buf(dx_out, "dx_out", shape, dev, xt), _buf(dy, "dy", shape, dev), _dt_of(dy), M, D,
+        _buf(dx, "dx", shape, dev, xt), _buf(dh, "dh", shape, dev, ht), _buf(dw_pre, "dw_pre", (D,), dev, _F32),
+        _buf(dw_post, "dw_post", (D,), dev, _F32), _buf(dgate, "dgate", (G, D), dev, _F32), wp, wb, _stream(stream)),
         "qlora_block_norm_bwd")
 
 
 def int8_quantize(x, codes, scales, stream=None) -> None:
     """Rows of x [rows, K] to int8 codes [rows, K] and fp32 scales [rows]."""
-    rows, K = x.shape
-    _check(LIB.int8_quantize(_buf(x, "x", x.shape), _dt(x.dtype), rows, K, _buf(codes, "codes", x.shape, _I8),
-                             _buf(scales, "scales", (rows,), _F32), _stream(stream)), "int8_quantize")
+    rows, K = shape = x.shape
+    dev = _device()
+    _check(LIB.int8_quantize(_buf(x, "x", shape, dev), _dt_of(x), rows, K, _buf(codes, "codes", shape, dev, _I8),
+                             _buf(scales, "scales", (rows,), dev, _F32), _stream(stream)), "int8_quantize")
 
 
 def int8_gemm(a_codes, a_scales, b_codes, b_scales, Y, ws=None, stream=None) -> None:
     """Y [M, N] = (a_codes [M, K] b_codes [N, K]^T) with the rows' scales; Y fp32 or bf16."""
     (M, K), N = a_codes.shape, b_codes.shape[0]
-    wp, wb = _ws(ws)
-    _check(LIB.int8_gemm(_buf(a_codes, "a_codes", (M, K), _I8), _buf(a_scales, "a_scales", (M,), _F32),
-                         _buf(b_codes, "b_codes", (N, K), _I8), _buf(b_scales, "b_scales", (N,), _F32), M, N, K,
-                         _buf(Y, "Y", (M, N)), _dt(Y.dtype), wp, wb, _stream(stream)), "int8_gemm")
+    dev = _device()
+    wp, wb = _ws(ws, dev)
+    _check(LIB.int8_gemm(_buf(a_codes, "a_codes", (M, K), dev, _I8), _buf(a_scales, "a_scales", (M,), dev, _F32),
+                         _buf(b_codes, "b_codes", (N, K), dev, _I8), _buf(b_scales, "b_scales", (N,), dev, _F32), M, N, K,
+                         _buf(Y, "Y", (M, N), dev), _dt_of(Y), wp, wb, _stream(stream)), "int8_gemm")
 
 
 # ------------------------------------------------------------- weight container

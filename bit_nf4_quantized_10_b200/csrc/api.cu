@@ -66,7 +66,6 @@ ql_status paged_prefetch(const void* ptr, size_t bytes, int where, cudaStream_t 
 // gradnorm.cu
 unsigned status_word_gradnorm(cudaStream_t st);
 size_t grad_norm_ws(int64_t count);
-int64_t grad_list_max_values();
 ql_status launch_grad_norm(const ql_tensor_list* list, float max_norm, float* norm, float* coef, void* ws,
                            cudaStream_t st);
 ql_status launch_grad_scale(const ql_tensor_list* list, const float* coef, cudaStream_t st);

@@ -17,6 +17,7 @@
 #include <cmath>
 
 #include "common.cuh"
+#include "sm100.cuh"
 #include "trace.cuh"
 
 namespace ql {
@@ -25,7 +26,10 @@ QL_DEFINE_STATUS_ACCESSOR(status_word_gradnorm)
 
 namespace gn {
 
-constexpr int kCap = 1024;       // tensors a launch: 20.5 KB of the 32 KB an argument list may have
+constexpr int kCap = 1024;       // most tensors a launch: 20.5 KB of the 32 KB an argument list may have
+constexpr int kFew = 32;         // lists up to here take a shorter argument list
+constexpr int kCluster = 8;      // blocks of the one-launch form
+constexpr uint32_t kSmallChunks = 64;   // it serves lists of up to so many chunks
 constexpr int kThreads = 256;
 constexpr int kChunk = 8192;     // values a block takes at a time
 
@@ -64,21 +68,18 @@ __device__ __forceinline__ double block_sum(double v, double* buf) {
   return v;
 }
 
+// A block's share of the sum of squares: every `step`-th chunk from `from` on.
 template <int CAP>
-__global__ void __launch_bounds__(kThreads) grad_sumsq_kernel(const __grid_constant__ List<CAP> l, double* parts) {
-  __shared__ double buf[kThreads / 32];
-  pdl_wait();
-  pdl_trigger();
+__device__ __forceinline__ double sum_chunks(const List<CAP>& l, uint32_t from, uint32_t step) {
   const int t = threadIdx.x;
   const uint32_t chunks = l.first[l.count];
   double acc[4] = {0.0, 0.0, 0.0, 0.0};
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+  for (uint32_t c = from; c < chunks; c += step) {
     const int i = tensor_of(l, c);
     const int64_t start = (int64_t)(c - l.first[i]) * kChunk;
     const int64_t left = l.numel[i] - start;
     const int len = left < kChunk ? (int)left : kChunk;
-    const bool is_bf16 = l.data[i] & 1;
-    if (is_bf16) {
+    if (l.data[i] & 1) {
       const __nv_bfloat16* g = reinterpret_cast<const __nv_bfloat16*>(l.data[i] & ~(uint64_t)1) + start;
       uint4 v[kChunk / 8 / kThreads];
 #pragma unroll
@@ -114,8 +115,16 @@ __global__ void __launch_bounds__(kThreads) grad_sumsq_kernel(const __grid_const
       if (tail < len) acc[0] = sq(acc[0], g[tail]);
     }
   }
-  const double s = block_sum((acc[0] + acc[1]) + (acc[2] + acc[3]), buf);
-  if (t == 0) parts[blockIdx.x] = s;
+  return (acc[0] + acc[1]) + (acc[2] + acc[3]);
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) grad_sumsq_kernel(const __grid_constant__ List<CAP> l, double* parts) {
+  __shared__ double buf[kThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  const double s = block_sum(sum_chunks(l, blockIdx.x, gridDim.x), buf);
+  if (threadIdx.x == 0) parts[blockIdx.x] = s;
 }
 
 __device__ __forceinline__ void write_norm(double sum, float max_norm, float* norm, float* coef) {
@@ -135,6 +144,33 @@ __global__ void __launch_bounds__(kThreads) grad_norm_finish_kernel(const double
   for (int i = threadIdx.x; i < count; i += kThreads) v += parts[i];
   v = block_sum(v, buf);
   if (threadIdx.x == 0) write_norm(v, max_norm, norm, coef);
+}
+
+// Small lists in one launch: a cluster of blocks whose sums the first block
+// reads from their shared memory.
+__global__ void __launch_bounds__(kThreads) grad_norm_small_kernel(const __grid_constant__ List<kFew> l, float max_norm,
+                                                                   float* norm, float* coef) {
+  __shared__ double buf[kThreads / 32];
+  __shared__ double mine;
+  pdl_wait();
+  pdl_trigger();
+  const double s = block_sum(sum_chunks(l, blockIdx.x, kCluster), buf);
+  if (threadIdx.x == 0) mine = s;
+  sm100::cluster_sync();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    double sum = 0.0;
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r) {
+      double part;
+      asm volatile("ld.shared::cluster.f64 %0, [%1];"
+                   : "=d"(part)
+                   : "r"(sm100::cluster_map(sm100::smem_u32(&mine), r))
+                   : "memory");
+      sum += part;
+    }
+    write_norm(sum, max_norm, norm, coef);
+  }
+  sm100::cluster_sync();   // no block leaves while its sum may still be read
 }
 
 template <int CAP>
@@ -217,32 +253,76 @@ int64_t fill(List<CAP>& l, const ql_tensor_list* in, int64_t at) {
   return at;
 }
 
+// One launch over the tensors from `at` on; `fn` is given the list and its grid.
+template <int CAP, typename F>
+ql_status one_launch(const ql_tensor_list* list, int64_t& at, F&& fn) {
+  List<CAP> l;
+  at = fill(l, list, at);
+  if (l.count == 0) return QL_OK;
+  TraceScope ts(TK_GRADNORM, fn.st);
+  return fn(l, (unsigned)std::min<int64_t>(l.first[l.count], max_blocks()));
+}
+
+struct SumLaunch {
+  cudaStream_t st;
+  double* parts;
+  int* used;
+  template <int CAP>
+  ql_status operator()(const List<CAP>& l, unsigned grid) const {
+    QL_CUDA_TRY(launch(grad_sumsq_kernel<CAP>, dim3(grid), dim3(kThreads), 0, st, 1, 1, l, parts + *used));
+    QL_LAUNCH_CHECK();
+    *used += (int)grid;
+    return QL_OK;
+  }
+};
+
+struct ScaleLaunch {
+  cudaStream_t st;
+  const float* coef;
+  template <int CAP>
+  ql_status operator()(const List<CAP>& l, unsigned grid) const {
+    QL_CUDA_TRY(launch(grad_scale_kernel<CAP>, dim3(grid), dim3(kThreads), 0, st, 1, 1, l, coef));
+    QL_LAUNCH_CHECK();
+    return QL_OK;
+  }
+};
+
+template <typename F>
+ql_status all_launches(const ql_tensor_list* list, F&& fn) {
+  for (int64_t at = 0; at < list->count;) {
+    const ql_status rc = list->count <= kFew ? one_launch<kFew>(list, at, fn) : one_launch<kCap>(list, at, fn);
+    if (rc != QL_OK) return rc;
+  }
+  return QL_OK;
+}
+
 }  // namespace gn
 
-// Slots for the blocks' sums: one launch for every kCap tensors (or 2^31
-// chunks, which a tensor of the largest size fills by itself).
+// Slots for the blocks' sums: one launch for every kCap tensors (a launch ends
+// earlier only past 2^31 chunks, more memory than a device has).
 size_t grad_norm_ws(int64_t count) {
   const int64_t launches = (count + gn::kCap - 1) / gn::kCap;
   return (size_t)std::max<int64_t>(launches, 1) * gn::max_blocks() * sizeof(double);
 }
 
-int64_t grad_list_max_values() { return (int64_t)gn::kChunk * 0x7FFFFFFF; }
-
 ql_status launch_grad_norm(const ql_tensor_list* list, float max_norm, float* norm, float* coef, void* ws,
                            cudaStream_t st) {
   using namespace gn;
+  if (list->count <= kFew) {
+    List<kFew> l;
+    fill(l, list, 0);
+    if (l.first[l.count] <= kSmallChunks) {
+      TraceScope ts(TK_GRADNORM, st);
+      QL_CUDA_TRY(launch(grad_norm_small_kernel, dim3(kCluster), dim3(kThreads), 0, st, kCluster, 1, l, max_norm, norm,
+                         coef));
+      QL_LAUNCH_CHECK();
+      return QL_OK;
+    }
+  }
   double* parts = reinterpret_cast<double*>(ws);
   int used = 0;
-  List<kCap> l;
-  for (int64_t at = 0; at < list->count;) {
-    at = fill(l, list, at);
-    if (l.count == 0) break;
-    const unsigned grid = (unsigned)std::min<int64_t>(l.first[l.count], max_blocks());
-    TraceScope ts(TK_GRADNORM, st);
-    QL_CUDA_TRY(launch(grad_sumsq_kernel<kCap>, dim3(grid), dim3(kThreads), 0, st, 1, 1, l, parts + used));
-    QL_LAUNCH_CHECK();
-    used += (int)grid;
-  }
+  const ql_status rc = all_launches(list, SumLaunch{st, parts, &used});
+  if (rc != QL_OK) return rc;
   TraceScope ts(TK_GRADNORM, st);
   QL_CUDA_TRY(launch(grad_norm_finish_kernel, dim3(1), dim3(kThreads), 0, st, 1, 1, (const double*)parts, used,
                      max_norm, norm, coef));
@@ -251,17 +331,7 @@ ql_status launch_grad_norm(const ql_tensor_list* list, float max_norm, float* no
 }
 
 ql_status launch_grad_scale(const ql_tensor_list* list, const float* coef, cudaStream_t st) {
-  using namespace gn;
-  List<kCap> l;
-  for (int64_t at = 0; at < list->count;) {
-    at = fill(l, list, at);
-    if (l.count == 0) break;
-    const unsigned grid = (unsigned)std::min<int64_t>(l.first[l.count], max_blocks());
-    TraceScope ts(TK_GRADNORM, st);
-    QL_CUDA_TRY(launch(grad_scale_kernel<kCap>, dim3(grid), dim3(kThreads), 0, st, 1, 1, l, coef));
-    QL_LAUNCH_CHECK();
-  }
-  return QL_OK;
+  return gn::all_launches(list, gn::ScaleLaunch{st, coef});
 }
 
 }  // namespace ql

@@ -262,6 +262,57 @@ __device__ __forceinline__ void block_sums(float (&s)[K], float* buf) {
     for (int d = 16; d; d >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], d);
   }
 }
+// Three sums over the block, one barrier.  Of four values (the last unused) a
+// lane first hands two to the lane 16 away and one to the lane 8 away, so each
+// quarter of the warp goes on with one value: 6 shuffles where three
+// separate sums take 15.
+__device__ __forceinline__ void block_sums3(float (&s)[3], float* buf) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const bool hi16 = lane & 16, hi8 = lane & 8;
+  // lanes 0-15 keep s0, s1; lanes 16-31 keep s2 (and nothing)
+  float a = (hi16 ? s[2] : s[0]) + __shfl_xor_sync(0xffffffffu, hi16 ? s[0] : s[2], 16);
+  float b = (hi16 ? 0.0f : s[1]) + __shfl_xor_sync(0xffffffffu, hi16 ? s[1] : 0.0f, 16);
+  // lanes 0-7: s0, 8-15: s1, 16-23: s2
+  float v = (hi8 ? b : a) + __shfl_xor_sync(0xffffffffu, hi8 ? a : b, 8);
+  v += __shfl_xor_sync(0xffffffffu, v, 4);
+  v += __shfl_xor_sync(0xffffffffu, v, 2);
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  if ((lane & 7) == 0) buf[(lane >> 3) * 32 + warp] = v;
+  __syncthreads();
+  const float* mine = buf + (lane >> 3) * 32;
+  v = 0.0f;
+  for (int w = lane & 7; w < warps; w += 8) v += mine[w];
+  v += __shfl_xor_sync(0xffffffffu, v, 4);
+  v += __shfl_xor_sync(0xffffffffu, v, 2);
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  s[0] = __shfl_sync(0xffffffffu, v, 0);
+  s[1] = __shfl_sync(0xffffffffu, v, 8);
+  s[2] = __shfl_sync(0xffffffffu, v, 16);
+}
+// Six sums over the block (two rows of three) the same way, for up to 16 warps:
+// an eighth of the warp goes on with each value, 9 shuffles before the barrier.
+__device__ __forceinline__ void block_sums6(float (&s)[6], float* buf) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const bool hi16 = lane & 16, hi8 = lane & 8, hi4 = lane & 4;
+  const float v[8] = {s[0], s[1], s[2], s[3], s[4], s[5], 0.0f, 0.0f};
+  float a[4], b[2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) a[j] = (hi16 ? v[4 + j] : v[j]) + __shfl_xor_sync(0xffffffffu, hi16 ? v[j] : v[4 + j], 16);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) b[j] = (hi8 ? a[2 + j] : a[j]) + __shfl_xor_sync(0xffffffffu, hi8 ? a[j] : a[2 + j], 8);
+  float c = (hi4 ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, hi4 ? b[0] : b[1], 4);
+  c += __shfl_xor_sync(0xffffffffu, c, 2);
+  c += __shfl_xor_sync(0xffffffffu, c, 1);
+  if ((lane & 3) == 0) buf[(lane >> 2) * 16 + warp] = c;
+  __syncthreads();
+  const float* mine = buf + (lane >> 2) * 16;
+  c = 0.0f;
+  for (int w = lane & 3; w < warps; w += 4) c += mine[w];
+  c += __shfl_xor_sync(0xffffffffu, c, 2);
+  c += __shfl_xor_sync(0xffffffffu, c, 1);
+#pragma unroll
+  for (int j = 0; j < 6; ++j) s[j] = __shfl_sync(0xffffffffu, c, 4 * j);
+}
 template <int K>
 __device__ __forceinline__ void warp_sums(float (&s)[K]) {
 #pragma unroll
@@ -601,7 +652,7 @@ __device__ __forceinline__ void add_sums(float* acc, int c, int D, const float (
 template <typename XT, typename HT, typename YT, int VPT, bool GROUPED>
 __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const BwdArgs a) {
   extern __shared__ __align__(16) float sums[];
-  __shared__ float red[2][3 * 32];
+  __shared__ float red[2][4 * 32];
   pdl_wait();
   pdl_trigger();
   const int t = threadIdx.x, nt = blockDim.x, D = a.D;
@@ -687,7 +738,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const BwdArgs a) 
         }
       }
       // dr = u - rsx c1 n with c1 = mean(dn n), so mean(dnh nh) = mean(u q) - rsx c1 mean(n q)
-      block_sums(s, red[parity]);
+      block_sums3(s, red[parity]);
       parity ^= 1;
       const float k1 = rsx * (s[0] * a.inv_d);
       const float c2 = (s[1] - k1 * s[2]) * a.inv_d;
@@ -749,8 +800,307 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const BwdArgs a) 
   }
 }
 
-// Adds the parts: 32 columns per block, its 8 warps take every 8th part each
-// and are added in order.  blockIdx.y: 0 dw_pre, 1 dw_post, 2 + g the gate g.
+// The same for many rows of a D that is a multiple of 8: the rows of a block's
+// chunks arrive by bulk copies in a ring of `stages` rows, and a thread owns the
+// same VPT groups of columns in every row.  All sums over a row go through one
+// barrier, after which its stage is free: by then the row is in registers.
+//   D <= 4096: one group a thread, R = 2 rows at a time, which share the barrier;
+//   gate (o + w_post), o + w_pre and the column sums stay in registers.
+//   D <= 8192: two groups, one row; 128 registers do not hold all of that, so the
+//   sum for dw_pre is in shared memory and w_pre is read again for every row.
+constexpr int kBwdStreamThreads = 512;
+
+// Eight columns of an array in shared memory, kept as two halves of four so that
+// neighbouring threads' 16-byte accesses are neighbours.
+__device__ __forceinline__ void lds8(const float* half, int D, int c, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(half + c / 2), b = *reinterpret_cast<const float4*>(half + D / 2 + c / 2);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void sts8(float* half, int D, int c, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(half + c / 2) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(half + D / 2 + c / 2) = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+template <typename XT, typename HT, typename YT, int VPT, int R, bool SUMS>
+__global__ void __launch_bounds__(kBwdStreamThreads) norm_bwd_stream_kernel(const BwdArgs a, int stages) {
+  extern __shared__ __align__(128) uint8_t dyn[];
+  __shared__ float red[2][4 * 32];
+  __shared__ uint64_t full_bar[kMaxStages];
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
+  const int t = threadIdx.x, nt = blockDim.x, D = a.D;
+  // a stage: x', dy, dx', h, those that are given
+  const int x_off = 0, y_off = a.dy ? D * (int)sizeof(XT) : 0, u_off = y_off + (a.dy ? D * (int)sizeof(YT) : 0),
+            h_off = u_off + (a.dx_out ? D * (int)sizeof(XT) : 0),
+            stage_bytes = h_off + (a.load_h ? D * (int)sizeof(HT) : 0);
+  float* acc_m = reinterpret_cast<float*>(dyn);      // VPT 2: the sums for dw_pre
+  uint8_t* ring = dyn + (VPT == 2 && SUMS && a.part_pre ? D * 4 : 0);
+  if (t == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&full_bar[s], 1);
+    abort_word = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+
+  // Rows of the block's chunks, one after the other.
+  struct Rows {
+    int64_t chunk, row, end, grp;
+  };
+  auto open = [&](Rows& r) {     // from r.chunk on, the first chunk with rows
+    for (; r.chunk < a.plan.chunks; r.chunk += gridDim.x) {
+      r.grp = r.chunk / a.plan.per_group;
+      r.row = r.grp * a.plan.group_rows + (r.chunk % a.plan.per_group) * a.plan.chunk_rows;
+      r.end = min(min(a.M, (r.grp + 1) * a.plan.group_rows), r.row + a.plan.chunk_rows);
+      if (r.row < r.end) return;
+    }
+  };
+  auto issue = [&](const Rows& r, int s) {
+    uint8_t* st = ring + (size_t)s * stage_bytes;
+    const int64_t flat = r.row * D;
+    mbar_arrive_expect_tx(&full_bar[s], (uint32_t)stage_bytes);
+    if (a.dy) {
+      bulk_load(st + x_off, reinterpret_cast<const XT*>(a.x) + flat, D * (uint32_t)sizeof(XT), &full_bar[s]);
+      bulk_load(st + y_off, reinterpret_cast<const YT*>(a.dy) + flat, D * (uint32_t)sizeof(YT), &full_bar[s]);
+    }
+    if (a.dx_out) bulk_load(st + u_off, reinterpret_cast<const XT*>(a.dx_out) + flat, D * (uint32_t)sizeof(XT), &full_bar[s]);
+    if (a.load_h) bulk_load(st + h_off, reinterpret_cast<const HT*>(a.h) + flat, D * (uint32_t)sizeof(HT), &full_bar[s]);
+  };
+  Rows ahead;                    // the next row to ask for (thread 0)
+  ahead.chunk = blockIdx.x;
+  if (t == 0) {
+    open(ahead);
+    for (int s = 0; s < stages && ahead.chunk < a.plan.chunks; ++s) {
+      issue(ahead, s);
+      if (++ahead.row == ahead.end) {
+        ahead.chunk += gridDim.x;
+        open(ahead);
+      }
+    }
+  }
+  float acc_s[VPT][8], gw[VPT][8], wp[8], acc_p[8];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc_s[k][j] = gw[k][j] = wp[j] = acc_p[j] = 0.0f;
+    const int c = (t + k * nt) * 8;
+    if (c >= D) continue;
+    if (VPT == 1 && a.dy) loadw8<true>(a.w_pre, a.w_f32, 0, D, c, D, a.offset, wp);
+    if (VPT == 2 && SUMS && a.part_pre) sts8(acc_m, D, c, acc_p);
+  }
+  const bool sum_s = SUMS && (a.part_post || a.part_s || a.dgate);
+  bool first = true;             // no chunk of this block has added to part_post
+  int s = 0, use = 0, parity = 0;
+  for (int64_t chunk = blockIdx.x; chunk < a.plan.chunks; chunk += gridDim.x) {
+    const int64_t grp = chunk / a.plan.per_group;
+    const int64_t row0 = grp * a.plan.group_rows + (chunk % a.plan.per_group) * a.plan.chunk_rows;
+    const int64_t row1 = min(min(a.M, (grp + 1) * a.plan.group_rows), row0 + a.plan.chunk_rows);
+    if (a.dh) {
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int c = (t + k * nt) * 8;
+        if (c >= D) continue;
+        float w[8];
+        loadw8<true>(a.w_post, a.w_f32, 0, D, c, D, a.w_post ? a.offset : 1.0f, w);
+        loadw8<true>(a.gate, a.w_f32, grp * D, a.gate_len, c, D, a.gate ? 0.0f : 1.0f, gw[k]);
+        mul8(gw[k], w);
+      }
+    }
+    // the rows' factors are asked for one step ahead
+    float rsx_next[R], rsh_next[R];
+    auto factors = [&](int64_t m) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int64_t row = min(m + r, row1 - 1);
+        rsx_next[r] = a.dy ? a.rstd_pre[row] : 0.0f;
+        rsh_next[r] = a.post ? a.rstd_post[row] : 1.0f;
+      }
+    };
+    if (row0 < row1) factors(row0);
+    for (int64_t m = row0; m < row1; m += R) {
+      float rsx[R], rsh[R], n[R][VPT][8], u[R][VPT][8], sum[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      Raw8<HT> hraw[R][VPT];         // h as loaded: 4 registers of bf16 where nh takes 8
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        rsx[r] = rsx_next[r];
+        rsh[r] = rsh_next[r];
+      }
+      if (m + R < row1) factors(m + R);
+      const int rows = (int)min((int64_t)R, row1 - m);
+      const int s_first = s;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r >= rows) break;
+        const uint8_t* st = ring + (size_t)s * stage_bytes;
+        mbar_wait(&full_bar[s], use & 1, abort_flag, 1u << 22);
+        if (++s == stages) {
+          s = 0;
+          ++use;
+        }
+        float d0 = 0.0f, d1 = 0.0f, e0 = 0.0f, e1 = 0.0f, f0 = 0.0f, f1 = 0.0f;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+          const int c = (t + k * nt) * 8;
+          if (c >= D) continue;
+          if (a.dx_out) {
+            Raw8<XT> raw;
+            raw.load(reinterpret_cast<const XT*>(st + u_off) + c);
+            raw.to_f32(u[r][k]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[r][k][j] = 0.0f;
+          }
+          if (a.dy) {
+            float dy[8];
+            Raw8<XT> raw;
+            raw.load(reinterpret_cast<const XT*>(st + x_off) + c);
+            raw.to_f32(n[r][k]);
+            Raw8<YT> yraw;
+            yraw.load(reinterpret_cast<const YT*>(st + y_off) + c);
+            yraw.to_f32(dy);
+            mul8(n[r][k], rsx[r]);
+            if (SUMS && a.part_pre) {
+              if (VPT == 1) {
+                fma8(acc_p, dy, n[r][k], acc_p);
+              } else {
+                float w[8];
+                lds8(acc_m, D, c, w);
+                fma8(w, dy, n[r][k], w);
+                sts8(acc_m, D, c, w);
+              }
+            }
+            if (VPT == 2) loadw8<true>(a.w_pre, a.w_f32, 0, D, c, D, a.offset, wp);
+            mul8(dy, wp);                                 // dn
+            dot8(d0, d1, dy, n[r][k]);
+            fma8(u[r][k], rsx[r], dy, u[r][k]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) n[r][k][j] = 0.0f;
+          }
+          if (a.load_h) {
+            hraw[r][k].load(reinterpret_cast<const HT*>(st + h_off) + c);
+            if (a.post) {
+              float q[8];
+              hraw[r][k].to_f32(q);
+              mul8(q, rsh[r]);
+              mul8(q, gw[k]);
+              dot8(e0, e1, u[r][k], q);
+              dot8(f0, f1, n[r][k], q);
+            }
+          }
+        }
+        sum[3 * r] = d0 + d1;
+        sum[3 * r + 1] = e0 + e1;
+        sum[3 * r + 2] = f0 + f1;
+      }
+      if constexpr (R == 1) {              // also: every thread has read the stages
+        float tot[3] = {sum[0], sum[1], sum[2]};
+        block_sums3(tot, red[parity]);
+        sum[0] = tot[0], sum[1] = tot[1], sum[2] = tot[2];
+      } else {
+        block_sums6(sum, red[parity]);
+      }
+      parity ^= 1;
+      if (t == 0) {
+        int free_s = s_first;
+        for (int r = 0; r < rows && ahead.chunk < a.plan.chunks; ++r) {
+          issue(ahead, free_s);
+          if (++free_s == stages) free_s = 0;
+          if (++ahead.row == ahead.end) {
+            ahead.chunk += gridDim.x;
+            open(ahead);
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r >= rows) break;
+        const int64_t flat = (m + r) * D;
+        const float k1 = rsx[r] * (sum[3 * r] * a.inv_d);
+        const float c2 = (sum[3 * r + 1] - k1 * sum[3 * r + 2]) * a.inv_d;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+          const int c = (t + k * nt) * 8;
+          if (c >= D) continue;
+          float (&dr)[8] = u[r][k];
+          fma8(dr, -k1, n[r][k], dr);
+          float nh[8];
+          if (a.load_h) {
+            hraw[r][k].to_f32(nh);
+            mul8(nh, rsh[r]);
+            if (SUMS && sum_s) fma8(acc_s[k], dr, nh, acc_s[k]);
+          }
+          if (a.dx) {
+            float o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = dr[j];
+            mul8(o, a.alpha);
+            store8_full(reinterpret_cast<XT*>(a.dx) + flat + c, o);
+          }
+          if (a.dh) {
+            mul8(dr, gw[k]);               // dnh
+            if (a.post) {
+              fma8(dr, -c2, nh, dr);
+              mul8(dr, rsh[r]);
+            }
+            store8_full(reinterpret_cast<HT*>(a.dh) + flat + c, dr);
+          }
+        }
+      }
+    }
+    if (SUMS && sum_s && a.gate) {         // a thread flushes the columns that it owns
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int c = (t + k * nt) * 8;
+        if (c >= D) continue;
+        float w[8];
+        if (a.part_post) {
+          float* dst = a.part_post + (int64_t)blockIdx.x * D + c;
+          loadw8<true>(a.gate, a.w_f32, grp * D, a.gate_len, c, D, 0.0f, w);
+          float old[8];
+          if (first) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) old[j] = 0.0f;
+          } else {
+            load8(dst, 0, 8, true, old);
+          }
+          fma8(old, w, acc_s[k], old);
+          store8_full(dst, old);
+        }
+        if (a.part_s) {
+          store8_full(a.part_s + chunk * D + c, acc_s[k]);
+        } else if (a.dgate) {
+          loadw8<true>(a.w_post, a.w_f32, 0, D, c, D, a.w_post ? a.offset : 1.0f, w);
+          mul8(w, acc_s[k]);
+          store8_full(a.dgate + grp * D + c, w);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc_s[k][j] = 0.0f;
+      }
+      first = false;
+    }
+  }
+  if (SUMS) {
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int c = (t + k * nt) * 8;
+      if (c >= D) continue;
+      if (a.part_pre) {
+        if (VPT == 2) lds8(acc_m, D, c, acc_p);
+        store8_full(a.part_pre + (int64_t)blockIdx.x * D + c, acc_p);
+      }
+      if (a.part_post && !a.gate) store8_full(a.part_post + (int64_t)blockIdx.x * D + c, acc_s[k]);
+    }
+  }
+}
+
+// Adds the parts in a fixed order: 32 columns per block, every warp takes each
+// 32nd part.  blockIdx.y 0: dw_pre; 1: dw_post, from its parts or from those of
+// S (a few gates); 2 + g: dgate's row g.
+constexpr int kFewGates = 8;
+
 struct FinishArgs {
   const float* part_pre;
   const float* part_post;
@@ -759,42 +1109,60 @@ struct FinishArgs {
   float* dw_post;
   float* dgate;
   const void* w_post;
+  const void* gate;
   int blocks;
-  int64_t per_group;
+  int64_t groups, per_group;
   int D;
   float offset;
   bool w_f32;
 };
 
-__global__ void __launch_bounds__(256) norm_finish_kernel(const FinishArgs a) {
-  __shared__ float part[8][32];
+__device__ __forceinline__ float value_at(const void* p, bool f32, int64_t i) {
+  return f32 ? reinterpret_cast<const float*>(p)[i] : to_f32(reinterpret_cast<const bf16*>(p)[i]);
+}
+
+// The sum over `parts` rows of src at this block's column `lane`, in warp 0.
+__device__ __forceinline__ float sum_parts(const float* src, int64_t parts, int c, int D, float (*buf)[33]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float s = 0.0f;
+  if (c < D)
+#pragma unroll 4
+    for (int64_t p = warp; p < parts; p += 32) s += src[p * D + c];
+  __syncthreads();          // the buffer's last use has been read
+  buf[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0) {
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) s += buf[w][lane];
+  }
+  return s;
+}
+
+__global__ void __launch_bounds__(1024) norm_finish_kernel(const FinishArgs a) {
+  __shared__ float buf[32][33];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  const float* src = blockIdx.y == 0 ? a.part_pre : a.part_post;
-  float* dst = blockIdx.y == 0 ? a.dw_pre : a.dw_post;
-  int64_t parts = a.blocks;
-  float scale = 1.0f;
-  if (blockIdx.y >= 2) {
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31);
+  const bool writes = threadIdx.x < 32 && c < a.D;
+  if (blockIdx.y == 0) {
+    if (!a.part_pre) return;
+    const float s = sum_parts(a.part_pre, a.blocks, c, a.D, buf);
+    if (writes) a.dw_pre[c] = s;
+  } else if (blockIdx.y >= 2) {
     const int64_t g = blockIdx.y - 2;
-    src = a.part_s + g * a.per_group * a.D;
-    dst = a.dgate + g * a.D;
-    parts = a.per_group;
-    if (a.w_post && c < a.D)
-      scale = a.offset + (a.w_f32 ? reinterpret_cast<const float*>(a.w_post)[c]
-                                  : to_f32(reinterpret_cast<const bf16*>(a.w_post)[c]));
-  }
-  if (!src) return;
-  float s = 0.0f;
-  if (c < a.D)
-    for (int64_t p = warp; p < parts; p += 8) s += src[p * a.D + c];
-  part[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && c < a.D) {
-#pragma unroll
-    for (int w = 1; w < 8; ++w) s += part[w][lane];
-    dst[c] = s * scale;
+    const float s = sum_parts(a.part_s + g * a.per_group * a.D, a.per_group, c, a.D, buf);
+    if (writes) a.dgate[g * a.D + c] = s * (a.w_post ? a.offset + value_at(a.w_post, a.w_f32, c) : 1.0f);
+  } else if (a.part_post) {
+    const float s = sum_parts(a.part_post, a.blocks, c, a.D, buf);
+    if (writes) a.dw_post[c] = s;
+  } else if (a.dw_post) {
+    float post = 0.0f;
+    for (int64_t g = 0; g < a.groups; ++g) {
+      const float s = sum_parts(a.part_s + g * a.per_group * a.D, a.per_group, c, a.D, buf);
+      if (writes) post += s * value_at(a.gate, a.w_f32, g * a.D + c);
+    }
+    if (writes) a.dw_post[c] = post;
   }
 }
 
@@ -809,13 +1177,22 @@ int groups_per_thread(int64_t D) {
 }
 unsigned row_threads(int64_t D, int vpt) { return (unsigned)((row_groups(D) + vpt * 32 - 1) / (vpt * 32) * 32); }
 
+int bwd_stream_vpt(int64_t D) { return D <= 8 * kBwdStreamThreads ? 1 : 2; }
+
+// Rows that fit two groups per thread and are more than the SMs take one of each.
+bool bwd_streams(int64_t M, int64_t D) {
+  const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
+  return D % 8 == 0 && D >= 512 && D <= 2 * 8 * kBwdStreamThreads && M > sms;
+}
+
 BwdPlan bwd_plan(int64_t M, int64_t D, int64_t gate_rows) {
   BwdPlan p;
   p.group_rows = gate_rows > 0 && gate_rows < M ? gate_rows : M;
   p.groups = (M + p.group_rows - 1) / p.group_rows;
   const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
-  const int threads = (int)row_threads(D, groups_per_thread(D));
-  const int per_sm = std::max(1, std::min(8, 640 / threads));
+  // blocks that an SM holds: of norm_bwd_stream_kernel at 128 registers, or of norm_bwd_kernel
+  const int per_sm = bwd_streams(M, D) ? std::max(1, kBwdStreamThreads / (int)row_threads(D, bwd_stream_vpt(D)))
+                                       : std::max(1, std::min(8, 640 / (int)row_threads(D, groups_per_thread(D))));
   const int64_t want = std::min<int64_t>(M, (int64_t)sms * per_sm);
   // Chunks per gate: the count whose slowest block has the fewest rows to go
   // through, a gate's chunk end counted as one row, over 1 to 8 chunks a block.
@@ -907,8 +1284,40 @@ ql_status run_bwd(const BwdArgs& a, size_t smem, cudaStream_t st) {
   return QL_OK;
 }
 
+template <typename XT, typename HT, typename YT, int VPT, bool SUMS>
+ql_status run_bwd_stream(const BwdArgs& a, cudaStream_t st) {
+  const auto kernel = norm_bwd_stream_kernel<XT, HT, YT, VPT, VPT == 1 ? 2 : 1, SUMS>;
+  constexpr int kMost = 220 * 1024;
+  if (per_device(reinterpret_cast<const void*>(kernel), 0, [kernel] {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess) {
+          cudaGetLastError();
+          return -1;
+        }
+        return 1;
+      }) < 0)
+    return QL_ERR_CUDA;
+  const int threads = (int)row_threads(a.D, VPT);
+  const int row = a.D * ((a.dy ? (int)(sizeof(XT) + sizeof(YT)) : 0) + (a.dx_out ? (int)sizeof(XT) : 0) +
+                         (a.load_h ? (int)sizeof(HT) : 0));
+  const int fixed = VPT == 2 && a.part_pre ? a.D * 4 : 0;
+  // rows under way: as many as fit beside the other blocks of an SM, at least one
+  const int share = kMost / std::max(1, kBwdStreamThreads / threads) - 2048;
+  const int stages = std::max(1, std::min(kMaxStages, (share - fixed) / row));
+  TraceScope ts(TK_NORM, st);
+  QL_CUDA_TRY(launch(kernel, dim3((unsigned)a.plan.blocks), dim3((unsigned)threads), (size_t)fixed + (size_t)stages * row,
+                     st, 1, 1, a, stages));
+  QL_LAUNCH_CHECK();
+  return QL_OK;
+}
+
 template <typename XT, typename HT, typename YT, bool GROUPED>
 ql_status pick_bwd(const BwdArgs& a, size_t smem, cudaStream_t st) {
+  if (GROUPED && bwd_streams(a.M, a.D)) {
+    const bool sums = a.part_pre || a.part_post || a.part_s || a.dgate;
+    if (bwd_stream_vpt(a.D) == 1)
+      return sums ? run_bwd_stream<XT, HT, YT, 1, true>(a, st) : run_bwd_stream<XT, HT, YT, 1, false>(a, st);
+    return sums ? run_bwd_stream<XT, HT, YT, 2, true>(a, st) : run_bwd_stream<XT, HT, YT, 2, false>(a, st);
+  }
   switch (groups_per_thread(a.D)) {
     case 1: return run_bwd<XT, HT, YT, 1, GROUPED>(a, smem, st);
     case 2: return run_bwd<XT, HT, YT, 2, GROUPED>(a, smem, st);
@@ -980,8 +1389,11 @@ ql_status launch_block_norm_bwd(const ql_block_norm* n, const void* x_out, ql_dt
   const size_t part = align256((size_t)a.plan.blocks * D * 4);
   uint8_t* wp = reinterpret_cast<uint8_t*>(ws);
   a.part_pre = dw_pre ? reinterpret_cast<float*>(wp) : nullptr;
-  a.part_post = dw_post ? reinterpret_cast<float*>(wp + part) : nullptr;
-  a.part_s = dgate && a.plan.per_group > 1 ? reinterpret_cast<float*>(wp + 2 * part) : nullptr;
+  // gates of several chunks leave S for dgate; from the S of a few gates
+  // dw_post follows too, with more of them every chunk adds to dw_post as it ends
+  const bool by_chunk = n->gate && a.plan.per_group > 1, few = by_chunk && a.plan.groups <= kFewGates;
+  a.part_post = dw_post && !few ? reinterpret_cast<float*>(wp + part) : nullptr;
+  a.part_s = (dgate && by_chunk) || (dw_post && few) ? reinterpret_cast<float*>(wp + 2 * part) : nullptr;
   a.x = x_out;
   a.h = h;
   a.dx_out = dx_out;
@@ -1004,7 +1416,7 @@ ql_status launch_block_norm_bwd(const ql_block_norm* n, const void* x_out, ql_dt
   a.post = h && n->w_post;
   a.load_h = (dh && a.post) || dw_post || dgate;
   const int64_t len = (D + 7) / 8 * 8;
-  const size_t smem = (size_t)len * 4 * ((dw_pre ? 1 : 0) + (dw_post || dgate ? 1 : 0) + (dw_post && n->gate ? 1 : 0));
+  const size_t smem = (size_t)len * 4 * ((dw_pre ? 1 : 0) + (dw_post || dgate ? 1 : 0) + (a.part_post && n->gate ? 1 : 0));
   const bool yf = dy && dy_dt == QL_F32;
   ql_status rc;
   if (x_dt == QL_F32)
@@ -1020,14 +1432,16 @@ ql_status launch_block_norm_bwd(const ql_block_norm* n, const void* x_out, ql_dt
   f.dw_post = dw_post;
   f.dgate = dgate;
   f.w_post = n->w_post;
+  f.gate = n->gate;
   f.blocks = a.plan.blocks;
+  f.groups = a.plan.groups;
   f.per_group = a.plan.per_group;
   f.D = (int)D;
   f.offset = n->w_offset;
   f.w_f32 = a.w_f32;
-  const dim3 grid((unsigned)((D + 31) / 32), 2u + (a.part_s ? (unsigned)a.plan.groups : 0u));
+  const dim3 grid((unsigned)((D + 31) / 32), 2u + (dgate && a.part_s ? (unsigned)a.plan.groups : 0u));
   TraceScope ts(TK_NORM, st);
-  QL_CUDA_TRY(launch(norm_finish_kernel, grid, dim3(256), 0, st, 1, 1, f));
+  QL_CUDA_TRY(launch(norm_finish_kernel, grid, dim3(1024), 0, st, 1, 1, f));
   QL_LAUNCH_CHECK();
   return QL_OK;
 }

@@ -125,11 +125,8 @@ def test_int8(lib):
 
 
 def test_binding_refuses_what_the_library_cannot_see(lib):
-    """Tensors on the CPU, of another shape or type, or not contiguous."""
+    """Tensors on the CPU, of another shape or type, or not contiguous (device -1 is the CPU's)."""
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
-    f32 = torch.zeros(4)
-    with pytest.raises(ValueError):
-        lib.int8_quantize(x, torch.zeros(4, 64, dtype=torch.int8), f32)
     with pytest.raises(ValueError):
         lib.TensorList([x])
     with pytest.raises(TypeError):
@@ -139,9 +136,13 @@ def test_binding_refuses_what_the_library_cannot_see(lib):
     with pytest.raises(ValueError):
         lib.BlockNorm(gate=torch.zeros(4, 4))
     with pytest.raises(ValueError):
-        lib._buf(x, "x", (4, 63))
-    with pytest.raises(TypeError):
-        lib._buf(x, "x", (4, 64), (torch.float32,))
+        lib._buf(x, "x", (4, 64), 0)
     with pytest.raises(ValueError):
-        lib._buf(x.t(), "x", (64, 4))
-    assert lib._buf(None, "x", (4, 4)) is None
+        lib._buf(x, "x", (4, 63), -1)
+    with pytest.raises(TypeError):
+        lib._buf(x, "x", (4, 64), -1, torch.float32)
+    with pytest.raises(ValueError):
+        lib._buf(x.t(), "x", (64, 4), -1)
+    with pytest.raises(TypeError):
+        lib._dt_of(torch.zeros(2, dtype=torch.float16))
+    assert lib._buf(None, "x", (4, 4), 0) is None and lib._buf(x, "x", (4, 64), -1) == x.data_ptr()
