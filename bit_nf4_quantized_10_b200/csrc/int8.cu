@@ -10,9 +10,10 @@
 // no more tensor-core time than it has to and the weight streams through
 // unchanged.  Two CTAs on two SMs share a tile (cta_group::2): each loads its
 // 128 weight rows and half of the tokens, 128 bytes of K per stage.
-//   warp 0      TMA producer (both CTAs)
-//   warp 1      even CTA: one thread issues the MMAs; odd CTA: one thread tells
-//               the even CTA which of its stages have landed
+//   warp 0      TMA producer (both CTAs); the copies of both complete on the even
+//               CTA's barrier of the stage (a thread of the odd CTA that passed
+//               its own barriers on took 1100 cycles a stage, twice the MMAs)
+//   warp 1      one thread of the even CTA issues the MMAs
 //   warps 2-5   drain one of the two accumulators (TMEM columns 0-255 and
 //               256-511) while the next tile fills the other
 // In the accumulator a TMEM lane is a weight row, so the 32 lanes of a warp
@@ -171,10 +172,10 @@ constexpr int BT = 256;                    // most tokens of a tile
 constexpr int BK = 128;                    // K values (bytes) of a stage
 constexpr int A_BYTES = BW / 2 * BK;       // 16 KB: a CTA's weight rows of a stage
 constexpr int MAX_STAGES = 8;
-constexpr int RING_BYTES = 196608;         // 6 stages at tn = 256
+constexpr int RING_BYTES = 7 * 32768;      // 7 stages at tn = 256
 constexpr int THREADS = 6 * 32;
 constexpr int TMEM_COLS = 512;
-constexpr size_t SMEM_BYTES = 1024 + RING_BYTES + 512;
+constexpr size_t SMEM_BYTES = RING_BYTES + 2 * BT * 4 + 256;   // 226.25 of the 227 KB that a block can have
 
 // Instruction descriptor, kind::i8: int32 D (2 at bit 4), int8 A and B (1 at
 // bits 7 and 10), both K-major, N >> 3 at bit 17, M >> 4 at bit 24, K = 32.
@@ -188,6 +189,16 @@ __device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, ui
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// TMA load of one CTA of a pair into its own shared memory that completes on a
+// barrier of the even CTA (no multicast).
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, uint32_t even_bar, int32_t x, int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(even_bar), "r"(x), "r"(y)
       : "memory");
 }
 
@@ -254,18 +265,32 @@ __device__ __forceinline__ void put_y(const Params& p, int64_t at, float v) {
     reinterpret_cast<float*>(p.Y)[at] = v;
 }
 
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+// Up to 16 tokens' values of one output channel (y points at the first; rows are N apart).
+template <typename T>
+__device__ __forceinline__ void put_column(T* y, int N, const float (&v)[16], int count) {
+  if (count >= 16) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) put(y + (int64_t)j * N, v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (j < count) put(y + (int64_t)j * N, v[j]);
+  }
+}
+
 __global__ void __launch_bounds__(THREADS, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                      const Params p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + RING_BYTES);   // a stage has landed in this CTA
-  uint64_t* peer = full + MAX_STAGES;                                // even CTA: it has landed in the odd one
-  uint64_t* empty = peer + MAX_STAGES;
+  extern __shared__ __align__(1024) uint8_t ring[];                  // the swizzle's atoms start on 1024 bytes
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + RING_BYTES);   // even CTA: a stage has landed in both
+  uint64_t* empty = full + MAX_STAGES;
   uint64_t* acc_full = empty + MAX_STAGES;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drained = acc_empty + 2;
-  uint32_t* tmem_addr = reinterpret_cast<uint32_t*>(drained + 1);
+  float* sa_tile = reinterpret_cast<float*>(drained + 2);            // [2][BT]
+  uint32_t* tmem_addr = reinterpret_cast<uint32_t*>(sa_tile + 2 * BT);
   volatile int* abort_flag = reinterpret_cast<int*>(tmem_addr + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1;
@@ -274,7 +299,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < MAX_STAGES; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&peer[i], 1);
       mbar_init(&empty[i], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -313,38 +337,31 @@ __global__ void __launch_bounds__(THREADS, 1)
             break;
           }
           uint8_t* st = ring + s * p.stage_bytes;
-          mbar_arrive_expect_tx(&full[s], (uint32_t)p.stage_bytes);
-          tma_load_2d(st, &map_w, &full[s], k * BK, wrow);
-          tma_load_2d(st + A_BYTES, &map_x, &full[s], k * BK, xrow);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)p.stage_bytes);
+          const uint32_t bar = cluster_map(smem_u32(&full[s]), 0);
+          tma_load_pair(st, &map_w, bar, k * BK, wrow);
+          tma_load_pair(st + A_BYTES, &map_x, bar, k * BK, xrow);
           ++n;
         }
       }
+      // a stage is empty once its copies have landed and the MMAs have read it:
       // no copy may still be landing, and no commit arriving, when the CTA exits
-      for (int i = n > S ? n - S : 0; i < n; ++i) {
-        mbar_wait(&full[i % S], (i / S) & 1, abort_flag, p.wait_limit);
-        if (ok) mbar_wait(&empty[i % S], (i / S) & 1, abort_flag, p.wait_limit);
-      }
+      for (int i = n > S ? n - S : 0; i < n; ++i) mbar_wait(&empty[i % S], (i / S) & 1, abort_flag, p.wait_limit);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       const uint32_t idesc = idesc_i8(BW, tn);
       int n = 0;
       bool ok = true;
       for (int i = 0; ok && work_at(p.plan, pair, i, w); ++i) {
         const int b = i & 1, use_b = i >> 1;
-        if (rank == 0 && use_b > 0) {
+        if (use_b > 0) {
           ok = mbar_wait_cluster(&acc_empty[b], (use_b - 1) & 1, abort_flag, p.wait_limit);
           tc_fence_after();
         }
         for (int k = w.k0; ok && k < w.k1; ++k, ++n) {
           const int s = n % S;
-          ok = mbar_wait(&full[s], (n / S) & 1, abort_flag, p.wait_limit);
-          if (!ok) break;
-          if (rank != 0) {
-            mbar_arrive_cluster(&peer[s], 0);
-            continue;
-          }
-          ok = mbar_wait_cluster(&peer[s], (n / S) & 1, abort_flag, p.wait_limit);
+          ok = mbar_wait_cluster(&full[s], (n / S) & 1, abort_flag, p.wait_limit);
           if (!ok) break;
           tc_fence_after();
           const uint32_t a_addr = smem_u32(ring + s * p.stage_bytes), b_addr = a_addr + A_BYTES;
@@ -354,43 +371,55 @@ __global__ void __launch_bounds__(THREADS, 1)
                         idesc, (k > w.k0 || kk > 0) ? 1u : 0u);
           mma_commit_pair(&empty[s]);
         }
-        if (rank == 0 && ok) mma_commit_pair(&acc_full[b]);
+        if (ok) mma_commit_pair(&acc_full[b]);
       }
-      if (rank == 0) {   // every MMA issued has completed before the pair frees its memory
-        mma_commit_pair_local(drained);
-        for (int i = 0; i < 4 && !mbar_try_wait(drained, 0); ++i) mbar_wait(drained, 0, abort_flag, p.wait_limit);
-      }
+      // every MMA issued has completed before the pair frees its memory
+      mma_commit_pair_local(drained);
+      for (int i = 0; i < 4 && !mbar_try_wait(drained, 0); ++i) mbar_wait(drained, 0, abort_flag, p.wait_limit);
     }
   } else {
-    const int quad = warp & 3;
+    const int quad = warp & 3, et = threadIdx.x - 64;
     const int in_tile = rank * (BW / 2) + quad * 32 + lane;   // weight row within the tile
     for (int i = 0; work_at(p.plan, pair, i, w); ++i) {
       const int b = i & 1;
-      const bool ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[b], (i >> 1) & 1, abort_flag, p.wait_limit) && !*abort_flag);
-      if (!ok) break;
-      tc_fence_after();
       const int n = w.tile / p.plan.token_tiles * BW + in_tile;
       const int m0 = w.tile % p.plan.token_tiles * tn;
       const int cols = min(tn, p.M - m0);
+      // the tokens' scales, while the accumulator fills; a warp comes here again
+      // for the same half only after the barrier of the other
+      float* sa = sa_tile + b * BT;
+      for (int c = et; c < tn; c += 128) sa[c] = c < cols ? p.sa[m0 + c] : 0.0f;
       const float sb = n < p.N ? p.sb[n] : 0.0f;
-      for (int c0 = 0; c0 < cols; c0 += 16) {
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[b], (i >> 1) & 1, abort_flag, p.wait_limit) && !*abort_flag);
+      if (!ok) *abort_flag = 1;     // the barrier above needs all four warps: keep going, without writing
+      tc_fence_after();
+      const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(b * BT);
+      uint32_t next[16];
+      tmem_ld16(acc, next);
+      for (int c0 = 0; c0 < cols && ok; c0 += 16) {
         uint32_t v[16];
-        tmem_ld16(tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(b * BT + c0), v);
         tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = next[j];
+        if (c0 + 16 < cols) tmem_ld16(acc + (uint32_t)(c0 + 16), next);
         if (w.slot >= 0) {
           int32_t* dst = p.parts + ((int64_t)w.slot * tn + c0) * BW + in_tile;
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             if (c0 + j < cols) dst[(int64_t)j * BW] = (int32_t)v[j];
         } else if (n < p.N) {
+          float y[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c0 + j < cols) {
-              const int64_t m = m0 + c0 + j;
-              put_y(p, m * p.N + n, __fmul_rn(__int2float_rn((int32_t)v[j]), __fmul_rn(p.sa[m], sb)));
-            }
+          for (int j = 0; j < 16; ++j) y[j] = __fmul_rn(__int2float_rn((int32_t)v[j]), __fmul_rn(sa[c0 + j], sb));
+          const int64_t at = (int64_t)(m0 + c0) * p.N + n;
+          if (p.y_bf16)
+            put_column(reinterpret_cast<__nv_bfloat16*>(p.Y) + at, p.N, y, cols - c0);
+          else
+            put_column(reinterpret_cast<float*>(p.Y) + at, p.N, y, cols - c0);
         }
       }
+      tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(&acc_empty[b], 0);
