@@ -43,8 +43,6 @@ bool make_map_2d(CUtensorMap* map, CUtensorMapDataType dt, int elem_bytes, const
 namespace i8 {
 
 // ------------------------------------------------------------------ quantize
-constexpr int kQThreads = 256;
-
 __device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -167,13 +165,14 @@ ql_status run_quant(const void* x, int64_t rows, int64_t K, int8_t* codes, float
 }
 
 // ------------------------------------------------------------------- product
-constexpr int BW = 256;                    // weight rows of a tile (128 per CTA)
+constexpr int BH = 256;                    // weight rows of an MMA (128 per CTA); a tile has H = 1 or 2 of them
 constexpr int BT = 256;                    // most tokens of a tile
 constexpr int BK = 128;                    // K values (bytes) of a stage
-constexpr int A_BYTES = BW / 2 * BK;       // 16 KB: a CTA's weight rows of a stage
-constexpr int MAX_STAGES = 8;
-constexpr int RING_BYTES = 7 * 32768;      // 7 stages at tn = 256
-constexpr int THREADS = 6 * 32;
+constexpr int A_BYTES = BH / 2 * BK;       // 16 KB: a CTA's rows of one half, one stage
+constexpr int MAX_STAGES = 12;
+constexpr int RING_BYTES = 7 * 32768;      // at tn = 256: 7 stages (H = 1) or 4 (H = 2)
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = (2 + EPI_WARPS) * 32;
 constexpr int TMEM_COLS = 512;
 constexpr size_t SMEM_BYTES = RING_BYTES + 2 * BT * 4 + 256;   // 226.25 of the 227 KB that a block can have
 
@@ -210,6 +209,7 @@ __device__ __forceinline__ void mma_commit_pair_local(uint64_t* bar) {
 
 // How the tiles are dealt to the pairs; the same on host and device.
 struct Plan {
+  int halves;          // H: 256-row halves of a tile
   int tn;              // tokens of a tile
   int token_tiles;
   int tiles;           // weight tiles x token tiles, token tiles fastest
@@ -253,7 +253,7 @@ struct Params {
   const float* sa;
   const float* sb;
   void* Y;
-  int32_t* parts;      // [2 rem_pairs][tn][BW]
+  int32_t* parts;      // [2 rem_pairs][tn][256 H]
   bool y_bf16;
   uint32_t wait_limit;
 };
@@ -280,6 +280,7 @@ __device__ __forceinline__ void put_column(T* y, int N, const float (&v)[16], in
   }
 }
 
+template <int H>
 __global__ void __launch_bounds__(THREADS, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                      const Params p) {
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 8);   // four warps of each CTA
+      mbar_init(&acc_empty[b], 2 * EPI_WARPS);   // of both CTAs
     }
     mbar_init(drained, 1);
     *abort_flag = 0;
@@ -325,104 +326,146 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (lane == 0) {
       prefetch_tmap(&map_w);
       prefetch_tmap(&map_x);
-      int n = 0;       // stages issued
+      // one thread issues every copy of a stage, so the loop is kept short: the
+      // ring's position is counted, not divided out
+      const uint32_t full0 = cluster_map(smem_u32(full), 0);   // the even CTA's barriers
+      int s = 0, use = 0;
       bool ok = true;
       for (int i = 0; ok && work_at(p.plan, pair, i, w); ++i) {
-        const int wrow = w.tile / p.plan.token_tiles * BW + rank * (BW / 2);
+        const int wrow = w.tile / p.plan.token_tiles * (BH * H) + rank * (BH / 2);
         const int xrow = w.tile % p.plan.token_tiles * tn + rank * (tn / 2);
         for (int k = w.k0; k < w.k1; ++k) {
-          const int s = n % S, use = n / S;
           if (use > 0 && !mbar_wait(&empty[s], (use - 1) & 1, abort_flag, p.wait_limit)) {
             ok = false;
             break;
           }
           uint8_t* st = ring + s * p.stage_bytes;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)p.stage_bytes);
-          const uint32_t bar = cluster_map(smem_u32(&full[s]), 0);
-          tma_load_pair(st, &map_w, bar, k * BK, wrow);
-          tma_load_pair(st + A_BYTES, &map_x, bar, k * BK, xrow);
-          ++n;
+#pragma unroll
+          for (int h = 0; h < H; ++h) tma_load_pair(st + h * A_BYTES, &map_w, full0 + 8u * s, k * BK, wrow + h * BH);
+          tma_load_pair(st + H * A_BYTES, &map_x, full0 + 8u * s, k * BK, xrow);
+          if (++s == S) {
+            s = 0;
+            ++use;
+          }
         }
       }
       // a stage is empty once its copies have landed and the MMAs have read it:
       // no copy may still be landing, and no commit arriving, when the CTA exits
-      for (int i = n > S ? n - S : 0; i < n; ++i) mbar_wait(&empty[i % S], (i / S) & 1, abort_flag, p.wait_limit);
+      for (int r = 0; r < S; ++r) {
+        if (use > 0) mbar_wait(&empty[s], (use - 1) & 1, abort_flag, p.wait_limit);
+        if (++s == S) {
+          s = 0;
+          ++use;
+        }
+      }
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      const uint32_t idesc = idesc_i8(BW, tn);
-      int n = 0;
+      const uint32_t idesc = idesc_i8(BH, tn);
+      const uint64_t a0 = sdesc_sw128(smem_u32(ring), 16, 1024);       // descriptors of stage 0; the
+      const uint64_t b0 = a0 + (uint64_t)(H * A_BYTES >> 4);           // address field counts 16 bytes
+      const uint32_t step = (uint32_t)p.stage_bytes >> 4;
+      int s = 0, use = 0;    // the next stage
       bool ok = true;
       for (int i = 0; ok && work_at(p.plan, pair, i, w); ++i) {
-        const int b = i & 1, use_b = i >> 1;
-        if (use_b > 0) {
-          ok = mbar_wait_cluster(&acc_empty[b], (use_b - 1) & 1, abort_flag, p.wait_limit);
-          tc_fence_after();
-        }
-        for (int k = w.k0; ok && k < w.k1; ++k, ++n) {
-          const int s = n % S;
-          ok = mbar_wait_cluster(&full[s], (n / S) & 1, abort_flag, p.wait_limit);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t a_addr = smem_u32(ring + s * p.stage_bytes), b_addr = a_addr + A_BYTES;
+        // H = 2: the first and the last stages of a tile go through as a group,
+        // all of half 0 and then all of half 1, so that half 0 is complete while
+        // the tensor cores still work on half 1, and is drained by the time the
+        // next tile's half 0 begins
+        const int steps = w.k1 - w.k0;
+        for (int k = 0; ok && k < steps;) {
+          const int group = H == 1 ? 1 : k == 0 ? min(S, steps) : steps - k <= S ? steps - k : 1;
+          int gs = s, gu = use;
 #pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk)
-            mma_i8_pair(tmem + b * BT, sdesc_sw128(a_addr + kk * 32, 16, 1024), sdesc_sw128(b_addr + kk * 32, 16, 1024),
-                        idesc, (k > w.k0 || kk > 0) ? 1u : 0u);
-          mma_commit_pair(&empty[s]);
+          for (int h = 0; h < H; ++h) {
+            const int q = i * H + h, b = q & 1, use_b = q >> 1;    // accumulator, and how often it was used
+            if (k == 0 && use_b > 0 && ok) {
+              ok = mbar_wait_cluster(&acc_empty[b], (use_b - 1) & 1, abort_flag, p.wait_limit);
+              tc_fence_after();
+            }
+            gs = s;
+            gu = use;
+            for (int g = 0; ok && g < group; ++g) {
+              if (h == 0) {
+                ok = mbar_wait(&full[gs], gu & 1, abort_flag, p.wait_limit);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              const uint64_t a = a0 + (uint64_t)(gs * step + h * (A_BYTES >> 4)), bd = b0 + (uint64_t)(gs * step);
+#pragma unroll
+              for (int kk = 0; kk < BK / 32; ++kk)
+                mma_i8_pair(tmem + b * BT, a + 2 * kk, bd + 2 * kk, idesc, (k + g > 0 || kk > 0) ? 1u : 0u);
+              if (h == H - 1) mma_commit_pair(&empty[gs]);
+              if (++gs == S) {
+                gs = 0;
+                ++gu;
+              }
+            }
+            if (ok && k + group == steps) mma_commit_pair(&acc_full[b]);
+          }
+          s = gs;
+          use = gu;
+          k += group;
         }
-        if (ok) mma_commit_pair(&acc_full[b]);
       }
       // every MMA issued has completed before the pair frees its memory
       mma_commit_pair_local(drained);
       for (int i = 0; i < 4 && !mbar_try_wait(drained, 0); ++i) mbar_wait(drained, 0, abort_flag, p.wait_limit);
     }
   } else {
-    const int quad = warp & 3, et = threadIdx.x - 64;
-    const int in_tile = rank * (BW / 2) + quad * 32 + lane;   // weight row within the tile
+    const int quad = warp & 3, et = threadIdx.x - 64, part = (warp - 2) >> 2;
+    int q = 0;
     for (int i = 0; work_at(p.plan, pair, i, w); ++i) {
-      const int b = i & 1;
-      const int n = w.tile / p.plan.token_tiles * BW + in_tile;
       const int m0 = w.tile % p.plan.token_tiles * tn;
       const int cols = min(tn, p.M - m0);
-      // the tokens' scales, while the accumulator fills; a warp comes here again
-      // for the same half only after the barrier of the other
-      float* sa = sa_tile + b * BT;
-      for (int c = et; c < tn; c += 128) sa[c] = c < cols ? p.sa[m0 + c] : 0.0f;
-      const float sb = n < p.N ? p.sb[n] : 0.0f;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      const bool ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[b], (i >> 1) & 1, abort_flag, p.wait_limit) && !*abort_flag);
-      if (!ok) *abort_flag = 1;     // the barrier above needs all four warps: keep going, without writing
-      tc_fence_after();
-      const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(b * BT);
-      uint32_t next[16];
-      tmem_ld16(acc, next);
-      for (int c0 = 0; c0 < cols && ok; c0 += 16) {
-        uint32_t v[16];
-        tmem_ld_wait();
+      // the tokens' scales, while the accumulator fills; nobody still reads this
+      // buffer, which served two tiles ago: all have passed the last tile's barrier
+      float* sa = sa_tile + (i & 1) * BT;
+      for (int c = et; c < tn; c += 32 * EPI_WARPS) sa[c] = c < cols ? p.sa[m0 + c] : 0.0f;
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * EPI_WARPS) : "memory");
+      // the two warps of a lane quarter take the first and the second half of the tokens
+      const int c_begin = part ? (tn / 2 + 15) / 16 * 16 : 0, c_end = part ? cols : min(cols, (tn / 2 + 15) / 16 * 16);
+#pragma unroll 1
+      for (int h = 0; h < H; ++h, ++q) {
+        const int b = q & 1;
+        const int in_tile = h * BH + rank * (BH / 2) + quad * 32 + lane;    // weight row within the tile
+        const int n = w.tile / p.plan.token_tiles * (BH * H) + in_tile;
+        const float sb = n < p.N ? p.sb[n] : 0.0f;
+        const bool ok =
+            __all_sync(0xffffffffu, mbar_wait(&acc_full[b], (q >> 1) & 1, abort_flag, p.wait_limit) && !*abort_flag);
+        if (!ok) *abort_flag = 1;     // the barrier above needs all warps: keep going, without writing
+        tc_fence_after();
+        const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(b * BT);
+        uint32_t next[16];
+        if (c_begin < c_end) tmem_ld16(acc + (uint32_t)c_begin, next);
+        for (int c0 = c_begin; c0 < c_end && ok; c0 += 16) {
+          uint32_t v[16];
+          tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = next[j];
-        if (c0 + 16 < cols) tmem_ld16(acc + (uint32_t)(c0 + 16), next);
-        if (w.slot >= 0) {
-          int32_t* dst = p.parts + ((int64_t)w.slot * tn + c0) * BW + in_tile;
+          for (int j = 0; j < 16; ++j) v[j] = next[j];
+          if (c0 + 16 < c_end) tmem_ld16(acc + (uint32_t)(c0 + 16), next);
+          if (w.slot >= 0) {
+            int32_t* dst = p.parts + ((int64_t)w.slot * tn + c0) * (BH * H) + in_tile;
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c0 + j < cols) dst[(int64_t)j * BW] = (int32_t)v[j];
-        } else if (n < p.N) {
-          float y[16];
+            for (int j = 0; j < 16; ++j)
+              if (c0 + j < cols) dst[(int64_t)j * (BH * H)] = (int32_t)v[j];
+          } else if (n < p.N) {
+            float y[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) y[j] = __fmul_rn(__int2float_rn((int32_t)v[j]), __fmul_rn(sa[c0 + j], sb));
-          const int64_t at = (int64_t)(m0 + c0) * p.N + n;
-          if (p.y_bf16)
-            put_column(reinterpret_cast<__nv_bfloat16*>(p.Y) + at, p.N, y, cols - c0);
-          else
-            put_column(reinterpret_cast<float*>(p.Y) + at, p.N, y, cols - c0);
+            for (int j = 0; j < 16; ++j) y[j] = __fmul_rn(__int2float_rn((int32_t)v[j]), __fmul_rn(sa[c0 + j], sb));
+            const int64_t at = (int64_t)(m0 + c0) * p.N + n;
+            if (p.y_bf16)
+              put_column(reinterpret_cast<__nv_bfloat16*>(p.Y) + at, p.N, y, cols - c0);
+            else
+              put_column(reinterpret_cast<float*>(p.Y) + at, p.N, y, cols - c0);
+          }
         }
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(&acc_empty[b], 0);
       }
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(&acc_empty[b], 0);
     }
   }
   tc_fence_before();
@@ -434,48 +477,82 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // Adds the part sums of the tiles that several pairs shared: a thread is a
-// weight row, blockIdx.x the tile, blockIdx.y deals the token columns.
-__global__ void __launch_bounds__(BW) int8_join_kernel(const Params p) {
-  pdl_wait();
-  pdl_trigger();
+// weight row, blockIdx.x the tile, blockIdx.y 8 of its tokens.
+constexpr int JOIN_TOKENS = 8;
+
+__global__ void __launch_bounds__(2 * BH) int8_join_kernel(const Params p) {
   const Plan& q = p.plan;
+  const int rows = blockDim.x;
   const int64_t lo = (int64_t)blockIdx.x * q.ksteps, hi = lo + q.ksteps;   // this tile's stages
+  // the pairs whose ranges [rem_steps r / rem_pairs, rem_steps (r + 1) / rem_pairs) meet them
   int first = (int)(lo * q.rem_pairs / q.rem_steps);
   while (first > 0 && q.rem_steps * first / q.rem_pairs > lo) --first;
   while (q.rem_steps * (first + 1) / q.rem_pairs <= lo) ++first;
-  const int64_t b0 = q.rem_steps * first / q.rem_pairs, e0 = q.rem_steps * (first + 1) / q.rem_pairs;
-  if (b0 <= lo && e0 >= hi) return;     // one pair had the whole tile and has written it
+  int last = first;
+  while (last + 1 < q.rem_pairs && q.rem_steps * (last + 1) / q.rem_pairs < hi) ++last;
+  const int64_t b0 = q.rem_steps * first / q.rem_pairs;
   const int tile = q.whole + blockIdx.x;
-  const int n = tile / q.token_tiles * BW + threadIdx.x, m0 = tile % q.token_tiles * q.tn;
-  if (n >= p.N) return;
-  const int cols = min(q.tn, p.M - m0);
-  const float sb = p.sb[n];
-  for (int c = blockIdx.y; c < cols; c += gridDim.y) {
-    int32_t acc = 0;
-    for (int r = first; r < q.rem_pairs; ++r) {
-      const int64_t b = q.rem_steps * r / q.rem_pairs;
-      if (b >= hi) break;
-      const int slot = r * 2 + (b < lo ? 1 : 0);
-      acc += p.parts[((int64_t)slot * q.tn + c) * BW + threadIdx.x];
-    }
-    const int64_t m = m0 + c;
-    put_y(p, m * p.N + n, __fmul_rn(__int2float_rn(acc), __fmul_rn(p.sa[m], sb)));
+  const int n = tile / q.token_tiles * rows + threadIdx.x, m0 = tile % q.token_tiles * q.tn;
+  const int c0 = blockIdx.y * JOIN_TOKENS, cols = min(JOIN_TOKENS, min(q.tn, p.M - m0) - c0);
+  pdl_wait();
+  pdl_trigger();
+  // a range that holds the whole tile has written it
+  if (n >= p.N || cols <= 0 || (first == last && b0 <= lo)) return;
+  const int64_t slot_size = (int64_t)q.tn * rows;
+  int32_t acc[JOIN_TOKENS] = {};
+  for (int r = first; r <= last; ++r) {
+    // the first range may have begun in the tile before: then this is its second part
+    const int64_t slot = 2 * r + (r == first && b0 < lo ? 1 : 0);
+    const int32_t* src = p.parts + slot * slot_size + (int64_t)c0 * rows + threadIdx.x;
+#pragma unroll
+    for (int c = 0; c < JOIN_TOKENS; ++c)
+      if (c < cols) acc[c] += src[(int64_t)c * rows];
   }
+  const float sb = p.sb[n];
+#pragma unroll
+  for (int c = 0; c < JOIN_TOKENS; ++c)
+    if (c < cols) {
+      const int64_t m = m0 + c0 + c;
+      put_y(p, m * p.N + n, __fmul_rn(__int2float_rn(acc[c]), __fmul_rn(p.sa[m], sb)));
+    }
 }
 
 Plan make_plan(int64_t M, int64_t N, int64_t K) {
   Plan p;
   p.token_tiles = (int)((M + BT - 1) / BT);
   p.tn = (int)(((M + p.token_tiles - 1) / p.token_tiles + 31) / 32 * 32);
-  p.tiles = (int)((N + BW - 1) / BW) * p.token_tiles;
   p.ksteps = (int)((K + BK - 1) / BK);
   p.pairs = std::max(1, (device_sm_count() > 0 ? device_sm_count() : 148) / 2);
+  // A stage feeds 256 H x tn x 128 products from 128 (256 H + tn) bytes.  At H = 1
+  // and tn = 256 the tensor cores want 64 bytes a cycle of each SM, more than L2
+  // delivers (40); H = 2 wants 48 but leaves one accumulator a half, so
+  // it is for tiles of many stages, several to a pair.
+  p.halves = p.tn > 128 && p.ksteps >= 16 && (N + 2 * BH - 1) / (2 * BH) * p.token_tiles >= 2 * p.pairs ? 2 : 1;
+  p.tiles = (int)((N + BH * p.halves - 1) / (BH * p.halves)) * p.token_tiles;
   p.whole = p.tiles / p.pairs * p.pairs;
   const int rem = p.tiles - p.whole;
   p.rem_steps = (int64_t)rem * p.ksteps;
   // a range of under 4 stages costs more to join than it saves
   p.rem_pairs = (int)std::min<int64_t>(p.pairs, std::max<int64_t>(rem, p.rem_steps / 4));
   return p;
+}
+
+template <int H>
+ql_status run_gemm(const CUtensorMap& map_w, const CUtensorMap& map_x, const Params& p, cudaStream_t st) {
+  if (per_device(reinterpret_cast<const void*>(int8_gemm_kernel<H>), 0, [] {
+        if (cudaFuncSetAttribute(int8_gemm_kernel<H>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES) !=
+            cudaSuccess) {
+          cudaGetLastError();
+          return -1;
+        }
+        return 1;
+      }) < 0)
+    return QL_ERR_CUDA;
+  const int active = p.plan.whole > 0 ? p.plan.pairs : p.plan.rem_pairs;
+  TraceScope ts(TK_INT8GEMM, st);
+  QL_CUDA_TRY(launch(int8_gemm_kernel<H>, dim3(2u * (unsigned)active), dim3(THREADS), SMEM_BYTES, st, 2, 1, map_w, map_x, p));
+  QL_LAUNCH_CHECK();
+  return QL_OK;
 }
 
 }  // namespace i8
@@ -487,7 +564,7 @@ size_t int8_gemm_ws(int64_t M, int64_t N, int64_t K) {
   const i8::Plan p = i8::make_plan(M, N, K);
   const int rem = p.tiles - p.whole;
   if (rem == 0 || p.rem_pairs == rem) return 0;   // every remaining tile has a pair to itself
-  return (size_t)p.rem_pairs * 2 * p.tn * i8::BW * 4;
+  return (size_t)p.rem_pairs * 2 * p.tn * i8::BH * p.halves * 4;
 }
 
 ql_status launch_int8_quantize(const void* x, ql_dtype dt, int64_t rows, int64_t K, int8_t* codes, float* scales,
@@ -499,26 +576,17 @@ ql_status launch_int8_quantize(const void* x, ql_dtype dt, int64_t rows, int64_t
 ql_status launch_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const float* sb, int64_t M, int64_t N,
                            int64_t K, void* Y, ql_dtype y_dt, void* ws, cudaStream_t st) {
   using namespace i8;
-  if (per_device(reinterpret_cast<const void*>(int8_gemm_kernel), 0, [] {
-        if (cudaFuncSetAttribute(int8_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES) !=
-            cudaSuccess) {
-          cudaGetLastError();
-          return -1;
-        }
-        return 1;
-      }) < 0)
-    return QL_ERR_CUDA;
   Params p;
   p.plan = make_plan(M, N, K);
   CUtensorMap map_w, map_x;
-  if (!make_map_2d(&map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, b, (uint64_t)K, (uint64_t)N, (uint64_t)K, BK, BW / 2,
+  if (!make_map_2d(&map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, b, (uint64_t)K, (uint64_t)N, (uint64_t)K, BK, BH / 2,
                    CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map_2d(&map_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a, (uint64_t)K, (uint64_t)M, (uint64_t)K, BK,
                    (uint32_t)p.plan.tn / 2, CU_TENSOR_MAP_SWIZZLE_128B))
     return QL_ERR_CUDA;
   p.M = (int)M;
   p.N = (int)N;
-  p.stage_bytes = A_BYTES + p.plan.tn / 2 * BK;
+  p.stage_bytes = p.plan.halves * A_BYTES + p.plan.tn / 2 * BK;
   p.stages = std::min(MAX_STAGES, RING_BYTES / p.stage_bytes);
   p.sa = sa;
   p.sb = sb;
@@ -526,17 +594,13 @@ ql_status launch_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, co
   p.parts = reinterpret_cast<int32_t*>(ws);
   p.y_bf16 = y_dt == QL_BF16;
   p.wait_limit = 1u << 22;
-  const int active = p.plan.whole > 0 ? p.plan.pairs : p.plan.rem_pairs;
-  {
-    TraceScope ts(TK_INT8GEMM, st);
-    QL_CUDA_TRY(launch(int8_gemm_kernel, dim3(2u * (unsigned)active), dim3(THREADS), SMEM_BYTES, st, 2, 1, map_w, map_x, p));
-    QL_LAUNCH_CHECK();
-  }
+  const ql_status rc = p.plan.halves == 2 ? run_gemm<2>(map_w, map_x, p, st) : run_gemm<1>(map_w, map_x, p, st);
+  if (rc != QL_OK) return rc;
   const int rem = p.plan.tiles - p.plan.whole;
   if (rem == 0 || p.plan.rem_pairs == rem) return QL_OK;
-  const unsigned deal = (unsigned)std::max(1, std::min(p.plan.tn, 592 / rem));
+  const unsigned deal = (unsigned)((std::min<int64_t>(p.plan.tn, M) + JOIN_TOKENS - 1) / JOIN_TOKENS);
   TraceScope ts(TK_INT8GEMM, st);
-  QL_CUDA_TRY(launch(int8_join_kernel, dim3((unsigned)rem, deal), dim3(BW), 0, st, 1, 1, p));
+  QL_CUDA_TRY(launch(int8_join_kernel, dim3((unsigned)rem, deal), dim3(BH * p.plan.halves), 0, st, 1, 1, p));
   QL_LAUNCH_CHECK();
   return QL_OK;
 }

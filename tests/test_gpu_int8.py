@@ -135,7 +135,8 @@ def test_reductions(q, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 19000, 1024), (8, 28672, 2048), (40, 18944, 640), (600, 8000, 512),
-                                   (1024, 19200, 256), (2500, 2300, 1040), (16, 37888, 128)])
+                                   (1024, 19200, 256), (2500, 2300, 1040), (16, 37888, 128),
+                                   (1024, 19200, 2064), (2100, 9001, 2048), (601, 28600, 2192), (2049, 8193, 2304)])
 def test_whole_rounds_and_shared_tiles(q, M, N, K):
     """Whole rounds of tiles, rounds and shared tiles, shared tiles alone."""
     _check(q, M, N, K)
