@@ -191,6 +191,21 @@ __device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
+// One lane of a converged warp.  The roles below are run by whole warps that
+// issue through this lane, so that descriptors and addresses stay in uniform
+// registers; run by one lane alone, every MMA and copy moves its operands there first.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit));
+}
+__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit) {
+  return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort, limit));
+}
+
 // TMA load of one CTA of a pair into its own shared memory that completes on a
 // barrier of the even CTA (no multicast).
 __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, uint32_t even_bar, int32_t x, int32_t y) {
@@ -293,7 +308,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   float* sa_tile = reinterpret_cast<float*>(drained + 2);            // [2][BT]
   uint32_t* tmem_addr = reinterpret_cast<uint32_t*>(sa_tile + 2 * BT);
   volatile int* abort_flag = reinterpret_cast<int*>(tmem_addr + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1;
   const int S = p.stages, tn = p.plan.tn;
 
@@ -323,9 +338,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   Work w;
   if (warp == 0) {
-    if (lane == 0) {
-      prefetch_tmap(&map_w);
-      prefetch_tmap(&map_x);
+    {
+      if (elect_one()) {
+        prefetch_tmap(&map_w);
+        prefetch_tmap(&map_x);
+      }
       // one thread issues every copy of a stage, so the loop is kept short: the
       // ring's position is counted, not divided out
       const uint32_t full0 = cluster_map(smem_u32(full), 0);   // the even CTA's barriers
@@ -335,15 +352,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int wrow = w.tile / p.plan.token_tiles * (BH * H) + rank * (BH / 2);
         const int xrow = w.tile % p.plan.token_tiles * tn + rank * (tn / 2);
         for (int k = w.k0; k < w.k1; ++k) {
-          if (use > 0 && !mbar_wait(&empty[s], (use - 1) & 1, abort_flag, p.wait_limit)) {
+          if (use > 0 && !warp_wait(&empty[s], (use - 1) & 1, abort_flag, p.wait_limit)) {
             ok = false;
             break;
           }
           uint8_t* st = ring + s * p.stage_bytes;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)p.stage_bytes);
+          if (elect_one()) {
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)p.stage_bytes);
 #pragma unroll
-          for (int h = 0; h < H; ++h) tma_load_pair(st + h * A_BYTES, &map_w, full0 + 8u * s, k * BK, wrow + h * BH);
-          tma_load_pair(st + H * A_BYTES, &map_x, full0 + 8u * s, k * BK, xrow);
+            for (int h = 0; h < H; ++h) tma_load_pair(st + h * A_BYTES, &map_w, full0 + 8u * s, k * BK, wrow + h * BH);
+            tma_load_pair(st + H * A_BYTES, &map_x, full0 + 8u * s, k * BK, xrow);
+          }
           if (++s == S) {
             s = 0;
             ++use;
@@ -353,7 +372,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // a stage is empty once its copies have landed and the MMAs have read it:
       // no copy may still be landing, and no commit arriving, when the CTA exits
       for (int r = 0; r < S; ++r) {
-        if (use > 0) mbar_wait(&empty[s], (use - 1) & 1, abort_flag, p.wait_limit);
+        if (use > 0) warp_wait(&empty[s], (use - 1) & 1, abort_flag, p.wait_limit);
         if (++s == S) {
           s = 0;
           ++use;
@@ -361,7 +380,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       const uint32_t idesc = idesc_i8(BH, tn);
       const uint64_t a0 = sdesc_sw128(smem_u32(ring), 16, 1024);       // descriptors of stage 0; the
       const uint64_t b0 = a0 + (uint64_t)(H * A_BYTES >> 4);           // address field counts 16 bytes
@@ -381,28 +400,30 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int h = 0; h < H; ++h) {
             const int q = i * H + h, b = q & 1, use_b = q >> 1;    // accumulator, and how often it was used
             if (k == 0 && use_b > 0 && ok) {
-              ok = mbar_wait_cluster(&acc_empty[b], (use_b - 1) & 1, abort_flag, p.wait_limit);
+              ok = warp_wait_cluster(&acc_empty[b], (use_b - 1) & 1, abort_flag, p.wait_limit);
               tc_fence_after();
             }
             gs = s;
             gu = use;
             for (int g = 0; ok && g < group; ++g) {
               if (h == 0) {
-                ok = mbar_wait(&full[gs], gu & 1, abort_flag, p.wait_limit);
+                ok = warp_wait(&full[gs], gu & 1, abort_flag, p.wait_limit);
                 if (!ok) break;
                 tc_fence_after();
               }
               const uint64_t a = a0 + (uint64_t)(gs * step + h * (A_BYTES >> 4)), bd = b0 + (uint64_t)(gs * step);
+              if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < BK / 32; ++kk)
-                mma_i8_pair(tmem + b * BT, a + 2 * kk, bd + 2 * kk, idesc, (k + g > 0 || kk > 0) ? 1u : 0u);
-              if (h == H - 1) mma_commit_pair(&empty[gs]);
+                for (int kk = 0; kk < BK / 32; ++kk)
+                  mma_i8_pair(tmem + b * BT, a + 2 * kk, bd + 2 * kk, idesc, (k + g > 0 || kk > 0) ? 1u : 0u);
+                if (h == H - 1) mma_commit_pair(&empty[gs]);
+              }
               if (++gs == S) {
                 gs = 0;
                 ++gu;
               }
             }
-            if (ok && k + group == steps) mma_commit_pair(&acc_full[b]);
+            if (ok && k + group == steps && elect_one()) mma_commit_pair(&acc_full[b]);
           }
           s = gs;
           use = gu;
@@ -410,8 +431,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       // every MMA issued has completed before the pair frees its memory
-      mma_commit_pair_local(drained);
-      for (int i = 0; i < 4 && !mbar_try_wait(drained, 0); ++i) mbar_wait(drained, 0, abort_flag, p.wait_limit);
+      if (elect_one()) mma_commit_pair_local(drained);
+      for (int i = 0; i < 4; ++i)
+        if (warp_wait(drained, 0, abort_flag, p.wait_limit)) break;
     }
   } else {
     const int quad = warp & 3, et = threadIdx.x - 64, part = (warp - 2) >> 2;
