@@ -11,18 +11,24 @@
 // unchanged.  Two CTAs on two SMs share a tile (cta_group::2): each loads its
 // 128 weight rows and half of the tokens, 128 bytes of K per stage.
 //   warp 0      TMA producer (both CTAs); the copies of both complete on the even
-//               CTA's barrier of the stage (a thread of the odd CTA that passed
-//               its own barriers on took 1100 cycles a stage, twice the MMAs)
-//   warp 1      one thread of the even CTA issues the MMAs
-//   warps 2-5   drain one of the two accumulators (TMEM columns 0-255 and
+//               CTA's barrier of the stage
+//   warp 1      even CTA: MMAs
+//   warps 2-9   drain one of the two accumulators (TMEM columns 0-255 and
 //               256-511) while the next tile fills the other
 // In the accumulator a TMEM lane is a weight row, so the 32 lanes of a warp
 // write 32 neighbouring values of a token's output row.
 //
+// The first two roles are run by whole warps that issue through an elected
+// lane: run by one lane alone, every MMA took its operands through general
+// registers, about 200 cycles each where N = 256 needs 128 (2048 tokens, 28672 x
+// 8192: 416 -> 355 us in that step).  What bounds it now: for
+// many tokens the tensor cores (83 % busy, then the power cap), in between the
+// 44 bytes a cycle that L2 feeds an SM, for a handful of tokens HBM.
+//
 // Work.  The pairs walk the tiles in rounds, token tiles fastest (the pairs at
-// work at a time share a few weight tiles in L2).  The tiles left over after
-// the whole rounds are cut along K into equal ranges, one per pair; a range
-// that is not a whole tile leaves its int32 sums in the workspace, and a second
+// work at a time share a few weight tiles in L2).  Where the tiles are so few
+// that most pairs would idle, each tile is cut along K into `splits` parts
+// with a pair for each; the int32 part sums go to the workspace and a second
 // kernel adds them.  Every wait is bounded (QL_ERR_TIMEOUT).
 #include <cudaTypedefs.h>
 
@@ -165,12 +171,12 @@ ql_status run_quant(const void* x, int64_t rows, int64_t K, int8_t* codes, float
 }
 
 // ------------------------------------------------------------------- product
-constexpr int BH = 256;                    // weight rows of an MMA (128 per CTA); a tile has H = 1 or 2 of them
+constexpr int BW = 256;                    // weight rows of a tile (128 per CTA)
 constexpr int BT = 256;                    // most tokens of a tile
 constexpr int BK = 128;                    // K values (bytes) of a stage
-constexpr int A_BYTES = BH / 2 * BK;       // 16 KB: a CTA's rows of one half, one stage
+constexpr int A_BYTES = BW / 2 * BK;       // 16 KB: a CTA's weight rows of a stage
 constexpr int MAX_STAGES = 12;
-constexpr int RING_BYTES = 7 * 32768;      // at tn = 256: 7 stages (H = 1) or 4 (H = 2)
+constexpr int RING_BYTES = 7 * 32768;      // 7 stages at tn = 256, 12 at tn = 32
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = (2 + EPI_WARPS) * 32;
 constexpr int TMEM_COLS = 512;
@@ -224,41 +230,30 @@ __device__ __forceinline__ void mma_commit_pair_local(uint64_t* bar) {
 
 // How the tiles are dealt to the pairs; the same on host and device.
 struct Plan {
-  int halves;          // H: 256-row halves of a tile
   int tn;              // tokens of a tile
   int token_tiles;
   int tiles;           // weight tiles x token tiles, token tiles fastest
   int ksteps;
-  int pairs;
-  int whole;           // tiles done in whole rounds (a multiple of `pairs`)
-  int rem_pairs;       // pairs that share the remaining tiles
-  int64_t rem_steps;   // stages of the remaining tiles together
+  int pairs;           // at work: min(tiles, SMs / 2), or tiles x splits
+  int splits;          // parts of K with a pair each; 1: whole tiles, in rounds
 };
 
 struct Work {
   int tile, k0, k1;
-  int slot;            // where the part sums go, or -1: the whole of K is here
 };
 
 __host__ __device__ inline bool work_at(const Plan& p, int pair, int i, Work& w) {
-  const int rounds = p.whole / p.pairs;
-  if (i < rounds) {
+  if (p.splits == 1) {
     w.tile = pair + i * p.pairs;
     w.k0 = 0;
     w.k1 = p.ksteps;
-    w.slot = -1;
-    return true;
+    return w.tile < p.tiles;
   }
-  i -= rounds;
-  if (pair >= p.rem_pairs || i > 1) return false;
-  const int64_t b = p.rem_steps * pair / p.rem_pairs, e = p.rem_steps * (pair + 1) / p.rem_pairs;
-  const int64_t t0 = b / p.ksteps + i, base = t0 * p.ksteps;
-  if (base >= e) return false;
-  w.tile = p.whole + (int)t0;
-  w.k0 = i ? 0 : (int)(b - base);
-  w.k1 = (int)(e - base < p.ksteps ? e - base : p.ksteps);
-  w.slot = w.k0 == 0 && w.k1 == p.ksteps ? -1 : pair * 2 + i;
-  return true;
+  const int part = pair % p.splits;
+  w.tile = pair / p.splits;
+  w.k0 = p.ksteps * part / p.splits;
+  w.k1 = p.ksteps * (part + 1) / p.splits;
+  return i == 0;
 }
 
 struct Params {
@@ -268,7 +263,7 @@ struct Params {
   const float* sa;
   const float* sb;
   void* Y;
-  int32_t* parts;      // [2 rem_pairs][tn][256 H]
+  int32_t* parts;      // [pairs][tn][BW], with splits
   bool y_bf16;
   uint32_t wait_limit;
 };
@@ -295,7 +290,6 @@ __device__ __forceinline__ void put_column(T* y, int N, const float (&v)[16], in
   }
 }
 
-template <int H>
 __global__ void __launch_bounds__(THREADS, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                      const Params p) {
@@ -349,7 +343,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       int s = 0, use = 0;
       bool ok = true;
       for (int i = 0; ok && work_at(p.plan, pair, i, w); ++i) {
-        const int wrow = w.tile / p.plan.token_tiles * (BH * H) + rank * (BH / 2);
+        const int wrow = w.tile / p.plan.token_tiles * BW + rank * (BW / 2);
         const int xrow = w.tile % p.plan.token_tiles * tn + rank * (tn / 2);
         for (int k = w.k0; k < w.k1; ++k) {
           if (use > 0 && !warp_wait(&empty[s], (use - 1) & 1, abort_flag, p.wait_limit)) {
@@ -359,9 +353,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint8_t* st = ring + s * p.stage_bytes;
           if (elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)p.stage_bytes);
-#pragma unroll
-            for (int h = 0; h < H; ++h) tma_load_pair(st + h * A_BYTES, &map_w, full0 + 8u * s, k * BK, wrow + h * BH);
-            tma_load_pair(st + H * A_BYTES, &map_x, full0 + 8u * s, k * BK, xrow);
+            tma_load_pair(st, &map_w, full0 + 8u * s, k * BK, wrow);
+            tma_load_pair(st + A_BYTES, &map_x, full0 + 8u * s, k * BK, xrow);
           }
           if (++s == S) {
             s = 0;
@@ -381,54 +374,35 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp == 1) {
     if (rank == 0) {
-      const uint32_t idesc = idesc_i8(BH, tn);
+      const uint32_t idesc = idesc_i8(BW, tn);
       const uint64_t a0 = sdesc_sw128(smem_u32(ring), 16, 1024);       // descriptors of stage 0; the
-      const uint64_t b0 = a0 + (uint64_t)(H * A_BYTES >> 4);           // address field counts 16 bytes
+      const uint64_t b0 = a0 + (uint64_t)(A_BYTES >> 4);               // address field counts 16 bytes
       const uint32_t step = (uint32_t)p.stage_bytes >> 4;
       int s = 0, use = 0;    // the next stage
       bool ok = true;
       for (int i = 0; ok && work_at(p.plan, pair, i, w); ++i) {
-        // H = 2: the first and the last stages of a tile go through as a group,
-        // all of half 0 and then all of half 1, so that half 0 is complete while
-        // the tensor cores still work on half 1, and is drained by the time the
-        // next tile's half 0 begins
-        const int steps = w.k1 - w.k0;
-        for (int k = 0; ok && k < steps;) {
-          const int group = H == 1 ? 1 : k == 0 ? min(S, steps) : steps - k <= S ? steps - k : 1;
-          int gs = s, gu = use;
-#pragma unroll
-          for (int h = 0; h < H; ++h) {
-            const int q = i * H + h, b = q & 1, use_b = q >> 1;    // accumulator, and how often it was used
-            if (k == 0 && use_b > 0 && ok) {
-              ok = warp_wait_cluster(&acc_empty[b], (use_b - 1) & 1, abort_flag, p.wait_limit);
-              tc_fence_after();
-            }
-            gs = s;
-            gu = use;
-            for (int g = 0; ok && g < group; ++g) {
-              if (h == 0) {
-                ok = warp_wait(&full[gs], gu & 1, abort_flag, p.wait_limit);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              const uint64_t a = a0 + (uint64_t)(gs * step + h * (A_BYTES >> 4)), bd = b0 + (uint64_t)(gs * step);
-              if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < BK / 32; ++kk)
-                  mma_i8_pair(tmem + b * BT, a + 2 * kk, bd + 2 * kk, idesc, (k + g > 0 || kk > 0) ? 1u : 0u);
-                if (h == H - 1) mma_commit_pair(&empty[gs]);
-              }
-              if (++gs == S) {
-                gs = 0;
-                ++gu;
-              }
-            }
-            if (ok && k + group == steps && elect_one()) mma_commit_pair(&acc_full[b]);
-          }
-          s = gs;
-          use = gu;
-          k += group;
+        const int b = i & 1, use_b = i >> 1;    // accumulator, and how often it was used
+        if (use_b > 0) {
+          ok = warp_wait_cluster(&acc_empty[b], (use_b - 1) & 1, abort_flag, p.wait_limit);
+          tc_fence_after();
         }
+        for (int k = w.k0; ok && k < w.k1; ++k) {
+          ok = warp_wait(&full[s], use & 1, abort_flag, p.wait_limit);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t a = a0 + (uint64_t)(s * step), bd = b0 + (uint64_t)(s * step);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < BK / 32; ++kk)
+              mma_i8_pair(tmem + b * BT, a + 2 * kk, bd + 2 * kk, idesc, (k > w.k0 || kk > 0) ? 1u : 0u);
+            mma_commit_pair(&empty[s]);
+          }
+          if (++s == S) {
+            s = 0;
+            ++use;
+          }
+        }
+        if (ok && elect_one()) mma_commit_pair(&acc_full[b]);
       }
       // every MMA issued has completed before the pair frees its memory
       if (elect_one()) mma_commit_pair_local(drained);
@@ -437,57 +411,53 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else {
     const int quad = warp & 3, et = threadIdx.x - 64, part = (warp - 2) >> 2;
-    int q = 0;
+    const int in_tile = rank * (BW / 2) + quad * 32 + lane;    // weight row within the tile
     for (int i = 0; work_at(p.plan, pair, i, w); ++i) {
+      const int b = i & 1;
+      const int n = w.tile / p.plan.token_tiles * BW + in_tile;
       const int m0 = w.tile % p.plan.token_tiles * tn;
       const int cols = min(tn, p.M - m0);
       // the tokens' scales, while the accumulator fills; nobody still reads this
       // buffer, which served two tiles ago: all have passed the last tile's barrier
-      float* sa = sa_tile + (i & 1) * BT;
+      float* sa = sa_tile + b * BT;
       for (int c = et; c < tn; c += 32 * EPI_WARPS) sa[c] = c < cols ? p.sa[m0 + c] : 0.0f;
+      const float sb = n < p.N ? p.sb[n] : 0.0f;
       asm volatile("bar.sync 1, %0;" ::"n"(32 * EPI_WARPS) : "memory");
       // the two warps of a lane quarter take the first and the second half of the tokens
-      const int c_begin = part ? (tn / 2 + 15) / 16 * 16 : 0, c_end = part ? cols : min(cols, (tn / 2 + 15) / 16 * 16);
-#pragma unroll 1
-      for (int h = 0; h < H; ++h, ++q) {
-        const int b = q & 1;
-        const int in_tile = h * BH + rank * (BH / 2) + quad * 32 + lane;    // weight row within the tile
-        const int n = w.tile / p.plan.token_tiles * (BH * H) + in_tile;
-        const float sb = n < p.N ? p.sb[n] : 0.0f;
-        const bool ok =
-            __all_sync(0xffffffffu, mbar_wait(&acc_full[b], (q >> 1) & 1, abort_flag, p.wait_limit) && !*abort_flag);
-        if (!ok) *abort_flag = 1;     // the barrier above needs all warps: keep going, without writing
-        tc_fence_after();
-        const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(b * BT);
-        uint32_t next[16];
-        if (c_begin < c_end) tmem_ld16(acc + (uint32_t)c_begin, next);
-        for (int c0 = c_begin; c0 < c_end && ok; c0 += 16) {
-          uint32_t v[16];
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = next[j];
-          if (c0 + 16 < c_end) tmem_ld16(acc + (uint32_t)(c0 + 16), next);
-          if (w.slot >= 0) {
-            int32_t* dst = p.parts + ((int64_t)w.slot * tn + c0) * (BH * H) + in_tile;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (c0 + j < cols) dst[(int64_t)j * (BH * H)] = (int32_t)v[j];
-          } else if (n < p.N) {
-            float y[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) y[j] = __fmul_rn(__int2float_rn((int32_t)v[j]), __fmul_rn(sa[c0 + j], sb));
-            const int64_t at = (int64_t)(m0 + c0) * p.N + n;
-            if (p.y_bf16)
-              put_column(reinterpret_cast<__nv_bfloat16*>(p.Y) + at, p.N, y, cols - c0);
-            else
-              put_column(reinterpret_cast<float*>(p.Y) + at, p.N, y, cols - c0);
-          }
-        }
+      const int c_begin = part ? tn / 2 : 0, c_end = part ? cols : min(cols, tn / 2);
+      const bool ok =
+          __all_sync(0xffffffffu, mbar_wait(&acc_full[b], (i >> 1) & 1, abort_flag, p.wait_limit) && !*abort_flag);
+      if (!ok) *abort_flag = 1;     // the barrier above needs all warps: keep going, without writing
+      tc_fence_after();
+      const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(b * BT);
+      uint32_t next[16];
+      if (c_begin < c_end) tmem_ld16(acc + (uint32_t)c_begin, next);
+      for (int c0 = c_begin; c0 < c_end && ok; c0 += 16) {
+        uint32_t v[16];
         tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(&acc_empty[b], 0);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = next[j];
+        if (c0 + 16 < c_end) tmem_ld16(acc + (uint32_t)(c0 + 16), next);
+        if (p.plan.splits > 1) {
+          int32_t* dst = p.parts + ((int64_t)pair * tn + c0) * BW + in_tile;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c0 + j < cols) dst[j * BW] = (int32_t)v[j];
+        } else if (n < p.N) {
+          float y[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) y[j] = __fmul_rn(__int2float_rn((int32_t)v[j]), __fmul_rn(sa[c0 + j], sb));
+          const int64_t at = (int64_t)(m0 + c0) * p.N + n;
+          if (p.y_bf16)
+            put_column(reinterpret_cast<__nv_bfloat16*>(p.Y) + at, p.N, y, cols - c0);
+          else
+            put_column(reinterpret_cast<float*>(p.Y) + at, p.N, y, cols - c0);
+        }
       }
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(&acc_empty[b], 0);
     }
   }
   tc_fence_before();
@@ -498,83 +468,75 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// Adds the part sums of the tiles that several pairs shared: a thread is a
-// weight row, blockIdx.x the tile, blockIdx.y 8 of its tokens.
-constexpr int JOIN_TOKENS = 8;
+// Adds the part sums of split tiles: a thread is a weight row, blockIdx.x the
+// tile, blockIdx.y JOIN_TOKENS of its tokens.
+constexpr int JOIN_TOKENS = 4;
 
-__global__ void __launch_bounds__(2 * BH) int8_join_kernel(const Params p) {
+__global__ void __launch_bounds__(BW) int8_join_kernel(const Params p) {
   const Plan& q = p.plan;
-  const int rows = blockDim.x;
-  const int64_t lo = (int64_t)blockIdx.x * q.ksteps, hi = lo + q.ksteps;   // this tile's stages
-  // the pairs whose ranges [rem_steps r / rem_pairs, rem_steps (r + 1) / rem_pairs) meet them
-  int first = (int)(lo * q.rem_pairs / q.rem_steps);
-  while (first > 0 && q.rem_steps * first / q.rem_pairs > lo) --first;
-  while (q.rem_steps * (first + 1) / q.rem_pairs <= lo) ++first;
-  int last = first;
-  while (last + 1 < q.rem_pairs && q.rem_steps * (last + 1) / q.rem_pairs < hi) ++last;
-  const int64_t b0 = q.rem_steps * first / q.rem_pairs;
-  const int tile = q.whole + blockIdx.x;
-  const int n = tile / q.token_tiles * rows + threadIdx.x, m0 = tile % q.token_tiles * q.tn;
+  const int n = blockIdx.x / q.token_tiles * BW + threadIdx.x, m0 = blockIdx.x % q.token_tiles * q.tn;
   const int c0 = blockIdx.y * JOIN_TOKENS, cols = min(JOIN_TOKENS, min(q.tn, p.M - m0) - c0);
   pdl_wait();
   pdl_trigger();
-  // a range that holds the whole tile has written it
-  if (n >= p.N || cols <= 0 || (first == last && b0 <= lo)) return;
-  const int64_t slot_size = (int64_t)q.tn * rows;
+  if (n >= p.N || cols <= 0) return;
+  const float sb = p.sb[n];
+  float scale[JOIN_TOKENS];
+#pragma unroll
+  for (int c = 0; c < JOIN_TOKENS; ++c) scale[c] = c < cols ? __fmul_rn(p.sa[m0 + c0 + c], sb) : 0.0f;
   int32_t acc[JOIN_TOKENS] = {};
-  for (int r = first; r <= last; ++r) {
-    // the first range may have begun in the tile before: then this is its second part
-    const int64_t slot = 2 * r + (r == first && b0 < lo ? 1 : 0);
-    const int32_t* src = p.parts + slot * slot_size + (int64_t)c0 * rows + threadIdx.x;
+  const int64_t part = (int64_t)q.tn * BW;
+  const int32_t* src = p.parts + blockIdx.x * (int64_t)q.splits * part + (int64_t)c0 * BW + threadIdx.x;
+#pragma unroll 4
+  for (int r = 0; r < q.splits; ++r) {
 #pragma unroll
     for (int c = 0; c < JOIN_TOKENS; ++c)
-      if (c < cols) acc[c] += src[(int64_t)c * rows];
+      if (c < cols) acc[c] += src[r * part + c * BW];
   }
-  const float sb = p.sb[n];
 #pragma unroll
   for (int c = 0; c < JOIN_TOKENS; ++c)
-    if (c < cols) {
-      const int64_t m = m0 + c0 + c;
-      put_y(p, m * p.N + n, __fmul_rn(__int2float_rn(acc[c]), __fmul_rn(p.sa[m], sb)));
-    }
+    if (c < cols) put_y(p, (int64_t)(m0 + c0 + c) * p.N + n, __fmul_rn(__int2float_rn(acc[c]), scale[c]));
 }
 
+// A plan's estimated cycles.  A stage takes the tensor cores 2 tn cycles and L2,
+// which feeds an SM 44 bytes a cycle, longer at small tn; the weight
+// comes from HBM at 23 bytes a cycle and SM, all of them together.  Joining costs
+// a launch (8000 cycles) and writing and reading the part sums, 1900 bytes a
+// cycle (fitted to 1 to 4096 tokens against weights of 300 x 4096 to 28672 x 8192).
+double plan_cycles(const Plan& p, int all_pairs) {
+  const double stage = std::max(2.0 * p.tn, (A_BYTES + p.tn * (BK / 2)) / 44.0);
+  const int steps = (p.ksteps + p.splits - 1) / p.splits;
+  const int rounds = (p.tiles * p.splits + all_pairs - 1) / all_pairs;
+  const double hbm = (double)p.tiles / p.token_tiles * p.ksteps * BW * BK / (2.0 * all_pairs * 23.0);
+  double c = std::max(rounds * steps * stage, hbm) + 10.0 * p.tn;
+  if (p.splits > 1) c += 8000.0 + 2.0 * p.pairs * p.tn * BW * 4.0 / 1900.0;
+  return c;
+}
+
+// Of a few token tile counts and, where one round leaves pairs idle, of the
+// splits that put them to work on at least 4 stages each, the plan with the
+// fewest cycles.
 Plan make_plan(int64_t M, int64_t N, int64_t K) {
-  Plan p;
-  p.token_tiles = (int)((M + BT - 1) / BT);
-  p.tn = (int)(((M + p.token_tiles - 1) / p.token_tiles + 31) / 32 * 32);
-  p.ksteps = (int)((K + BK - 1) / BK);
-  p.pairs = std::max(1, (device_sm_count() > 0 ? device_sm_count() : 148) / 2);
-  // A stage feeds 256 H x tn x 128 products from 128 (256 H + tn) bytes.  At H = 1
-  // and tn = 256 the tensor cores want 64 bytes a cycle of each SM, more than L2
-  // delivers (40); H = 2 wants 48 but leaves one accumulator a half, so
-  // it is for tiles of many stages, several to a pair.
-  p.halves = p.tn > 128 && p.ksteps >= 16 && (N + 2 * BH - 1) / (2 * BH) * p.token_tiles >= 2 * p.pairs ? 2 : 1;
-  p.tiles = (int)((N + BH * p.halves - 1) / (BH * p.halves)) * p.token_tiles;
-  p.whole = p.tiles / p.pairs * p.pairs;
-  const int rem = p.tiles - p.whole;
-  p.rem_steps = (int64_t)rem * p.ksteps;
-  // a range of under 4 stages costs more to join than it saves
-  p.rem_pairs = (int)std::min<int64_t>(p.pairs, std::max<int64_t>(rem, p.rem_steps / 4));
-  return p;
-}
-
-template <int H>
-ql_status run_gemm(const CUtensorMap& map_w, const CUtensorMap& map_x, const Params& p, cudaStream_t st) {
-  if (per_device(reinterpret_cast<const void*>(int8_gemm_kernel<H>), 0, [] {
-        if (cudaFuncSetAttribute(int8_gemm_kernel<H>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES) !=
-            cudaSuccess) {
-          cudaGetLastError();
-          return -1;
-        }
-        return 1;
-      }) < 0)
-    return QL_ERR_CUDA;
-  const int active = p.plan.whole > 0 ? p.plan.pairs : p.plan.rem_pairs;
-  TraceScope ts(TK_INT8GEMM, st);
-  QL_CUDA_TRY(launch(int8_gemm_kernel<H>, dim3(2u * (unsigned)active), dim3(THREADS), SMEM_BYTES, st, 2, 1, map_w, map_x, p));
-  QL_LAUNCH_CHECK();
-  return QL_OK;
+  Plan best{};
+  double least = 0.0;
+  const int all_pairs = std::max(1, (device_sm_count() > 0 ? device_sm_count() : 148) / 2);
+  const int64_t fewest = (M + BT - 1) / BT;
+  for (int64_t tt = fewest; tt <= fewest + 2; ++tt) {
+    Plan p;
+    p.ksteps = (int)((K + BK - 1) / BK);
+    p.tn = (int)(((M + tt - 1) / tt + 31) / 32 * 32);
+    p.token_tiles = (int)((M + p.tn - 1) / p.tn);
+    p.tiles = (int)((N + BW - 1) / BW) * p.token_tiles;
+    const int most = std::max(1, std::min(all_pairs / p.tiles, p.ksteps / 4));
+    for (p.splits = 1; p.splits <= most; ++p.splits) {
+      p.pairs = p.splits > 1 ? p.tiles * p.splits : std::min(p.tiles, all_pairs);
+      const double c = plan_cycles(p, all_pairs);
+      if (least == 0.0 || c < least) {
+        least = c;
+        best = p;
+      }
+    }
+  }
+  return best;
 }
 
 }  // namespace i8
@@ -584,9 +546,7 @@ int64_t int8_max_k() { return 131056; }   // the largest multiple of 16 whose su
 size_t int8_gemm_ws(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K <= 0 || M >= ((int64_t)1 << 31) || N >= ((int64_t)1 << 31) || K > int8_max_k()) return 0;
   const i8::Plan p = i8::make_plan(M, N, K);
-  const int rem = p.tiles - p.whole;
-  if (rem == 0 || p.rem_pairs == rem) return 0;   // every remaining tile has a pair to itself
-  return (size_t)p.rem_pairs * 2 * p.tn * i8::BH * p.halves * 4;
+  return p.splits > 1 ? (size_t)p.pairs * p.tn * i8::BW * 4 : 0;
 }
 
 ql_status launch_int8_quantize(const void* x, ql_dtype dt, int64_t rows, int64_t K, int8_t* codes, float* scales,
@@ -598,17 +558,26 @@ ql_status launch_int8_quantize(const void* x, ql_dtype dt, int64_t rows, int64_t
 ql_status launch_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const float* sb, int64_t M, int64_t N,
                            int64_t K, void* Y, ql_dtype y_dt, void* ws, cudaStream_t st) {
   using namespace i8;
+  if (per_device(reinterpret_cast<const void*>(int8_gemm_kernel), 0, [] {
+        if (cudaFuncSetAttribute(int8_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES) !=
+            cudaSuccess) {
+          cudaGetLastError();
+          return -1;
+        }
+        return 1;
+      }) < 0)
+    return QL_ERR_CUDA;
   Params p;
   p.plan = make_plan(M, N, K);
   CUtensorMap map_w, map_x;
-  if (!make_map_2d(&map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, b, (uint64_t)K, (uint64_t)N, (uint64_t)K, BK, BH / 2,
+  if (!make_map_2d(&map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, b, (uint64_t)K, (uint64_t)N, (uint64_t)K, BK, BW / 2,
                    CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map_2d(&map_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a, (uint64_t)K, (uint64_t)M, (uint64_t)K, BK,
                    (uint32_t)p.plan.tn / 2, CU_TENSOR_MAP_SWIZZLE_128B))
     return QL_ERR_CUDA;
   p.M = (int)M;
   p.N = (int)N;
-  p.stage_bytes = p.plan.halves * A_BYTES + p.plan.tn / 2 * BK;
+  p.stage_bytes = A_BYTES + p.plan.tn / 2 * BK;
   p.stages = std::min(MAX_STAGES, RING_BYTES / p.stage_bytes);
   p.sa = sa;
   p.sb = sb;
@@ -616,13 +585,13 @@ ql_status launch_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, co
   p.parts = reinterpret_cast<int32_t*>(ws);
   p.y_bf16 = y_dt == QL_BF16;
   p.wait_limit = 1u << 22;
-  const ql_status rc = p.plan.halves == 2 ? run_gemm<2>(map_w, map_x, p, st) : run_gemm<1>(map_w, map_x, p, st);
-  if (rc != QL_OK) return rc;
-  const int rem = p.plan.tiles - p.plan.whole;
-  if (rem == 0 || p.plan.rem_pairs == rem) return QL_OK;
-  const unsigned deal = (unsigned)((std::min<int64_t>(p.plan.tn, M) + JOIN_TOKENS - 1) / JOIN_TOKENS);
   TraceScope ts(TK_INT8GEMM, st);
-  QL_CUDA_TRY(launch(int8_join_kernel, dim3((unsigned)rem, deal), dim3(BH * p.plan.halves), 0, st, 1, 1, p));
+  QL_CUDA_TRY(launch(int8_gemm_kernel, dim3(2u * (unsigned)p.plan.pairs), dim3(THREADS), SMEM_BYTES, st, 2, 1, map_w,
+                     map_x, p));
+  QL_LAUNCH_CHECK();
+  if (p.plan.splits == 1) return QL_OK;
+  const unsigned deal = (unsigned)((std::min<int64_t>(p.plan.tn, M) + JOIN_TOKENS - 1) / JOIN_TOKENS);
+  QL_CUDA_TRY(launch(int8_join_kernel, dim3((unsigned)p.plan.tiles, deal), dim3(BW), 0, st, 1, 1, p));
   QL_LAUNCH_CHECK();
   return QL_OK;
 }
