@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(BW) int8_join_kernel(const Params p) {
 // A plan's estimated cycles.  A stage takes the tensor cores 2 tn cycles and L2,
 // which feeds an SM 44 bytes a cycle, longer at small tn; the weight
 // comes from HBM at 23 bytes a cycle and SM, all of them together.  Joining costs
-// a launch (8000 cycles) and writing and reading the part sums, 1900 bytes a
+// a launch (7000 cycles) and writing and reading the part sums, 1900 bytes a
 // cycle (fitted to 1 to 4096 tokens against weights of 300 x 4096 to 28672 x 8192).
 double plan_cycles(const Plan& p, int all_pairs) {
   const double stage = std::max(2.0 * p.tn, (A_BYTES + p.tn * (BK / 2)) / 44.0);
@@ -508,7 +508,7 @@ double plan_cycles(const Plan& p, int all_pairs) {
   const int rounds = (p.tiles * p.splits + all_pairs - 1) / all_pairs;
   const double hbm = (double)p.tiles / p.token_tiles * p.ksteps * BW * BK / (2.0 * all_pairs * 23.0);
   double c = std::max(rounds * steps * stage, hbm) + 10.0 * p.tn;
-  if (p.splits > 1) c += 8000.0 + 2.0 * p.pairs * p.tn * BW * 4.0 / 1900.0;
+  if (p.splits > 1) c += 7000.0 + 2.0 * p.pairs * p.tn * BW * 4.0 / 1900.0;
   return c;
 }
 
