@@ -49,6 +49,26 @@ class GradBucket:
     def allreduce(self, group=None) -> None:
         dist.all_reduce(self.buffer, op=dist.ReduceOp.SUM, group=group)
 
+    def clip(self, max_norm: float, scale: bool = True):
+        """The global norm of the bucket's gradients and the coefficient
+        min(1, max_norm / (norm + 1e-6)), as fp32 device tensors [1]; with `scale`
+        the gradients are multiplied by it in place.  Without, the caller hands
+        the coefficient to qlora_adamw_step_clipped, which needs no pass over
+        the gradients of its own.  After allreduce() every rank gets the same
+        bits.  The padding between the views is zero and stays out of the norm.
+        The tensors are the bucket's own and are overwritten by the next call."""
+        from . import _lib as L
+        if not hasattr(self, "_list"):
+            self._list = L.TensorList([self.buffer])
+            self._norm = torch.empty(2, 4, dtype=torch.float32, device=self.buffer.device)   # 16 bytes each
+            need = L.qlora_workspace_size(L.QL_OP_GRAD_NORM, 1)
+            self._ws = torch.empty(max(need, 16), dtype=torch.uint8, device=self.buffer.device)
+        norm, coef = self._norm[0, :1], self._norm[1, :1]
+        L.qlora_grad_norm(self._list, max_norm, norm, coef, self._ws)
+        if scale:
+            L.qlora_grad_scale(self._list, coef)
+        return norm, coef
+
 
 def allreduce_adapter_grads(dA: torch.Tensor, dB: torch.Tensor, group=None) -> None:
     """Sum dA and dB over the ranks in place (every rank gets the total), as

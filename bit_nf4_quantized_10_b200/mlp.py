@@ -6,6 +6,9 @@ a 65B Model on One GPU", "Seeing it in code": gate_proj, up_proj, down_proj);
 the block is the usual gated MLP  y = Ld(silu(Lg(x)) * Lu(x)).
 g, u and h are materialized as bf16; dX of the gate and up linears are summed
 in fp32 (accumulate_dx), and dX is returned in fp32.
+
+QLoRAMLPStack puts such MLPs into residual blocks with norms before and after;
+MergedInt8MLP is the 8-bit serving form of one after training.
 """
 from __future__ import annotations
 
@@ -60,6 +63,19 @@ class QLoRAMLP:
         q.qlora_linear_bwd(self.wu, X, self.du, self.Au, self.Bu, r, s, self.Uu, self.dX, self.dAu, self.dBu,
                            accumulate_dx=True, ws=ws)
 
+    def use_gradients(self, views) -> None:
+        """Write the adapter gradients into these six fp32 tensors (dAg, dBg, dAu, dBu, dAd, dBd), as a GradBucket
+        of gradient_shapes() hands them out."""
+        for name, v in zip(self.GRADIENTS, views, strict=True):
+            if v.shape != getattr(self, name).shape:
+                raise ValueError(f"{name}: shape {tuple(v.shape)} instead of {tuple(getattr(self, name).shape)}")
+            setattr(self, name, v)
+
+    GRADIENTS = ("dAg", "dBg", "dAu", "dBu", "dAd", "dBd")
+
+    def gradient_shapes(self):
+        return [tuple(getattr(self, name).shape) for name in self.GRADIENTS]
+
     def flops(self) -> float:
         M, r = self.M, self.r
         tot = 0.0
@@ -67,3 +83,110 @@ class QLoRAMLP:
             N, K = w.rows, w.cols
             tot += 4.0 * M * N * K + 6.0 * M * r * (K + N)
         return tot
+
+
+class QLoRAMLPStack:
+    """Residual blocks around QLoRA MLPs, with the norms between them fused:
+
+        y_0 = pre_norm_0(x_0)
+        h_i = MLP_i(y_i),  x_{i+1} = alpha x_i + gate_i post_norm_i(h_i),  y_{i+1} = pre_norm_{i+1}(x_{i+1})
+
+    `norms` holds one BlockNorm more than there are MLPs: norms[0] is the norm in
+    front of the first block (w_pre alone), norms[i + 1] the post norm and gate of
+    block i and, as its w_pre, the norm of what comes next (a further block, or
+    the head; w_pre may be None after the last block).  Everything is kept for
+    the backward pass: M tokens of D channels, the stream in `stream_dtype`.
+    With train_norms, backward() also writes dw_pre, dw_post and dgate (fp32,
+    lists by norm, None where a norm has no such weight)."""
+
+    def __init__(self, mlps, norms, stream_dtype=torch.bfloat16, train_norms: bool = False):
+        if len(norms) != len(mlps) + 1:
+            raise ValueError("one norm more than MLPs")
+        if norms[0].w_pre is None or norms[0].w_post is not None or norms[0].gate is not None or norms[0].alpha != 1.0:
+            raise ValueError("the first norm has no block in front of it: w_pre alone, alpha 1")
+        if any(n.w_pre is None for n in norms[:-1]):
+            raise ValueError("every norm but the last feeds a block and needs w_pre")
+        self.mlps, self.norms = list(mlps), list(norms)
+        L, M, D, dev = len(mlps), mlps[0].M, mlps[0].wg.cols, mlps[0].Ag.device
+        bf, f32 = torch.bfloat16, torch.float32
+        new = lambda *shape, dt=f32: torch.empty(*shape, dtype=dt, device=dev)  # noqa: E731
+        self.x = [None] + [new(M, D, dt=stream_dtype) for _ in range(L)]
+        self.y = [new(M, D, dt=bf) if n.w_pre is not None else None for n in norms]
+        self.h = [new(M, D, dt=bf) for _ in range(L)]
+        self.rstd_pre = [new(M) for _ in norms]
+        self.rstd_post = [new(M) for _ in norms]
+        self.dx, self.dh = new(M, D, dt=stream_dtype), new(M, D, dt=bf)
+        sums = lambda t, shape: new(*shape) if train_norms and t is not None else None  # noqa: E731
+        self.dw_pre = [sums(n.w_pre, (D,)) for n in norms]
+        self.dw_post = [sums(n.w_post, (D,)) for n in norms]
+        self.dgate = [sums(n.gate, n.gate.shape if n.gate is not None else ()) for n in norms]
+        need = max(q.qlora_workspace_size(q.QL_OP_BLOCK_NORM_BWD, M, D, n.gate_rows if n.gate is not None else 0)
+                   for n in norms)
+        self.ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+
+    def forward(self, x):
+        """x [M, D] of the stream's type, kept until backward(); returns the last stream and the last norm's output."""
+        self.x[0] = x
+        q.qlora_block_norm_fwd(self.norms[0], x, None, None, self.y[0], self.rstd_pre[0])
+        for i, mlp in enumerate(self.mlps):
+            mlp.forward(self.y[i], self.h[i])
+            q.qlora_block_norm_fwd(self.norms[i + 1], self.x[i], self.h[i], self.x[i + 1], self.y[i + 1],
+                                   self.rstd_pre[i + 1], self.rstd_post[i + 1])
+        return self.x[-1], self.y[-1]
+
+    def backward(self, dx_out, dy_out):
+        """Gradients of <dx_out, stream> + <dy_out, normed output> (either may be None); returns the input's."""
+        dx, dy = dx_out, dy_out
+        for i in reversed(range(len(self.mlps))):
+            j = i + 1
+            q.qlora_block_norm_bwd(self.norms[j], self.x[j], self.h[i], self.rstd_pre[j], self.rstd_post[j], dx, dy,
+                                   self.dx, self.dh, dw_pre=self.dw_pre[j] if dy is not None else None,
+                                   dw_post=self.dw_post[j], dgate=self.dgate[j], ws=self.ws)
+            self.mlps[i].backward(self.y[i], self.dh)
+            dx, dy = self.dx, self.mlps[i].dX
+        q.qlora_block_norm_bwd(self.norms[0], self.x[0], None, self.rstd_pre[0], None, dx, dy, self.dx, None,
+                               dw_pre=self.dw_pre[0], ws=self.ws)
+        return self.dx
+
+
+class MergedInt8MLP:
+    """The gated MLP with its adapters merged and its weights in 8 bits, one scale
+    per output channel; every linear quantizes its tokens on the way in.  Up to
+    `M` tokens a call; forward only (the merged weights are not trained)."""
+
+    def __init__(self, mlp: QLoRAMLP, M: int):
+        dev = mlp.Ag.device
+        self.M = M
+        self.weights = []
+        for w, A, B in ((mlp.wg, mlp.Ag, mlp.Bg), (mlp.wu, mlp.Au, mlp.Bu), (mlp.wd, mlp.Ad, mlp.Bd)):
+            merged = torch.empty(w.rows, w.cols, dtype=torch.bfloat16, device=dev)
+            q.qlora_merge(w, A, B, mlp.r, mlp.s, W_out=merged)
+            codes = torch.empty(w.rows, w.cols, dtype=torch.int8, device=dev)
+            scales = torch.empty(w.rows, dtype=torch.float32, device=dev)
+            q.int8_quantize(merged, codes, scales)
+            self.weights.append((codes, scales))
+        H, D = mlp.wg.rows, mlp.wg.cols
+        self.x_codes = torch.empty(M, D, dtype=torch.int8, device=dev)
+        self.h_codes = torch.empty(M, H, dtype=torch.int8, device=dev)
+        self.scales = torch.empty(M, dtype=torch.float32, device=dev)
+        self.g, self.u, self.h = (torch.empty(M, H, dtype=torch.bfloat16, device=dev) for _ in range(3))
+        # the plan of a product depends on its number of tokens: room for any up to M
+        need = max(q.qlora_workspace_size(q.QL_OP_INT8_GEMM, m, n, k) for m in range(1, M + 1)
+                   for n, k in ((H, D), (D, H)))
+        self.ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+
+    def forward(self, x, y) -> None:
+        """y [m, D] (fp32 or bf16) from x [m, D] (bf16 or fp32), m <= M."""
+        m = x.shape[0]
+        if m > self.M:
+            raise ValueError(f"{m} tokens, room for {self.M}")
+        (wg, sg), (wu, su), (wd, sd) = self.weights
+        xc, hc, s, g, u, h = (t[:m] for t in (self.x_codes, self.h_codes, self.scales, self.g, self.u, self.h))
+        if m == 0:
+            return
+        q.int8_quantize(x, xc, s)
+        q.int8_gemm(xc, s, wg, sg, g, ws=self.ws)
+        q.int8_gemm(xc, s, wu, su, u, ws=self.ws)
+        q.qlora_silu_gate_fwd(g, u, h)
+        q.int8_quantize(h, hc, s)
+        q.int8_gemm(hc, s, wd, sd, y, ws=self.ws)
