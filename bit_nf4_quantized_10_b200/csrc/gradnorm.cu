@@ -29,6 +29,7 @@ namespace gn {
 constexpr int kCap = 1024;       // most tensors a launch: 20.5 KB of the 32 KB an argument list may have
 constexpr int kFew = 32;         // lists up to here take a shorter argument list
 constexpr int kCluster = 8;      // blocks of the one-launch form
+constexpr int kSmallThreads = 1024;     // and their threads
 constexpr uint32_t kSmallChunks = 64;   // it serves lists of up to so many chunks
 constexpr int kThreads = 256;
 constexpr int kChunk = 8192;     // values a block takes at a time
@@ -57,6 +58,7 @@ __device__ __forceinline__ double sq(double acc, float v) {
   return fma(d, d, acc);
 }
 
+template <int THREADS>
 __device__ __forceinline__ double block_sum(double v, double* buf) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
@@ -64,12 +66,12 @@ __device__ __forceinline__ double block_sum(double v, double* buf) {
   __syncthreads();
   v = 0.0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) v += buf[w];
+  for (int w = 0; w < THREADS / 32; ++w) v += buf[w];
   return v;
 }
 
 // A block's share of the sum of squares: every `step`-th chunk from `from` on.
-template <int CAP>
+template <int THREADS, int CAP>
 __device__ __forceinline__ double sum_chunks(const List<CAP>& l, uint32_t from, uint32_t step) {
   const int t = threadIdx.x;
   const uint32_t chunks = l.first[l.count];
@@ -81,14 +83,14 @@ __device__ __forceinline__ double sum_chunks(const List<CAP>& l, uint32_t from, 
     const int len = left < kChunk ? (int)left : kChunk;
     if (l.data[i] & 1) {
       const __nv_bfloat16* g = reinterpret_cast<const __nv_bfloat16*>(l.data[i] & ~(uint64_t)1) + start;
-      uint4 v[kChunk / 8 / kThreads];
+      uint4 v[kChunk / 8 / THREADS];
 #pragma unroll
-      for (int k = 0; k < kChunk / 8 / kThreads; ++k) {
-        const int e = (k * kThreads + t) * 8;
+      for (int k = 0; k < kChunk / 8 / THREADS; ++k) {
+        const int e = (k * THREADS + t) * 8;
         v[k] = e + 8 <= len ? *reinterpret_cast<const uint4*>(g + e) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int k = 0; k < kChunk / 8 / kThreads; ++k) {
+      for (int k = 0; k < kChunk / 8 / THREADS; ++k) {
         acc[0] = sq(sq(acc[0], bf16_lo(v[k].x)), bf16_hi(v[k].x));
         acc[1] = sq(sq(acc[1], bf16_lo(v[k].y)), bf16_hi(v[k].y));
         acc[2] = sq(sq(acc[2], bf16_lo(v[k].z)), bf16_hi(v[k].z));
@@ -98,14 +100,14 @@ __device__ __forceinline__ double sum_chunks(const List<CAP>& l, uint32_t from, 
       if (tail < len) acc[0] = sq(acc[0], __bfloat162float(g[tail]));
     } else {
       const float* g = reinterpret_cast<const float*>(l.data[i]) + start;
-      float4 v[kChunk / 4 / kThreads];
+      float4 v[kChunk / 4 / THREADS];
 #pragma unroll
-      for (int k = 0; k < kChunk / 4 / kThreads; ++k) {
-        const int e = (k * kThreads + t) * 4;
+      for (int k = 0; k < kChunk / 4 / THREADS; ++k) {
+        const int e = (k * THREADS + t) * 4;
         v[k] = e + 4 <= len ? *reinterpret_cast<const float4*>(g + e) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
-      for (int k = 0; k < kChunk / 4 / kThreads; ++k) {
+      for (int k = 0; k < kChunk / 4 / THREADS; ++k) {
         acc[0] = sq(acc[0], v[k].x);
         acc[1] = sq(acc[1], v[k].y);
         acc[2] = sq(acc[2], v[k].z);
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(kThreads) grad_sumsq_kernel(const __grid_const
   __shared__ double buf[kThreads / 32];
   pdl_wait();
   pdl_trigger();
-  const double s = block_sum(sum_chunks(l, blockIdx.x, gridDim.x), buf);
+  const double s = block_sum<kThreads>(sum_chunks<kThreads>(l, blockIdx.x, gridDim.x), buf);
   if (threadIdx.x == 0) parts[blockIdx.x] = s;
 }
 
@@ -142,19 +144,19 @@ __global__ void __launch_bounds__(kThreads) grad_norm_finish_kernel(const double
   pdl_trigger();
   double v = 0.0;
   for (int i = threadIdx.x; i < count; i += kThreads) v += parts[i];
-  v = block_sum(v, buf);
+  v = block_sum<kThreads>(v, buf);
   if (threadIdx.x == 0) write_norm(v, max_norm, norm, coef);
 }
 
 // Small lists in one launch: a cluster of blocks whose sums the first block
 // reads from their shared memory.
-__global__ void __launch_bounds__(kThreads) grad_norm_small_kernel(const __grid_constant__ List<kFew> l, float max_norm,
+__global__ void __launch_bounds__(kSmallThreads) grad_norm_small_kernel(const __grid_constant__ List<kFew> l, float max_norm,
                                                                    float* norm, float* coef) {
-  __shared__ double buf[kThreads / 32];
+  __shared__ double buf[kSmallThreads / 32];
   __shared__ double mine;
   pdl_wait();
   pdl_trigger();
-  const double s = block_sum(sum_chunks(l, blockIdx.x, kCluster), buf);
+  const double s = block_sum<kSmallThreads>(sum_chunks<kSmallThreads>(l, blockIdx.x, kCluster), buf);
   if (threadIdx.x == 0) mine = s;
   sm100::cluster_sync();
   if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -313,7 +315,7 @@ ql_status launch_grad_norm(const ql_tensor_list* list, float max_norm, float* no
     fill(l, list, 0);
     if (l.first[l.count] <= kSmallChunks) {
       TraceScope ts(TK_GRADNORM, st);
-      QL_CUDA_TRY(launch(grad_norm_small_kernel, dim3(kCluster), dim3(kThreads), 0, st, kCluster, 1, l, max_norm, norm,
+      QL_CUDA_TRY(launch(grad_norm_small_kernel, dim3(kCluster), dim3(kSmallThreads), 0, st, kCluster, 1, l, max_norm, norm,
                          coef));
       QL_LAUNCH_CHECK();
       return QL_OK;

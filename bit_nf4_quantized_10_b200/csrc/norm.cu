@@ -18,6 +18,7 @@
 // is.  A row of a D that is no multiple of 8 starts and ends inside a group;
 // only those edge groups are accessed element by element.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "sm100.cuh"
@@ -321,6 +322,10 @@ __device__ __forceinline__ void warp_sums(float (&s)[K]) {
     for (int d = 16; d; d >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], d);
 }
 
+__device__ __forceinline__ float value_at(const void* p, bool f32, int64_t i) {
+  return f32 ? reinterpret_cast<const float*>(p)[i] : to_f32(reinterpret_cast<const bf16*>(p)[i]);
+}
+
 struct FwdArgs {
   const void* x;
   const void* h;
@@ -622,14 +627,16 @@ struct BwdArgs {
   BwdPlan plan;
 };
 
-// Where column c's sum is kept.  GROUPED: groups of 8 as two halves of four, so
-// that a thread's two 16-byte accesses meet no bank conflict.  Otherwise
-// neighbouring threads hold columns 8 apart: columns with equal c % 8 are
-// neighbours.
+// Where column c's sum is kept, so that neighbouring threads, whose columns are 8
+// apart, meet no bank conflict.  GROUPED: groups of 8 as two halves of four, for
+// a thread's two 16-byte accesses.  Otherwise one value in 32 is left free.
 template <bool GROUPED>
-__device__ __forceinline__ int sum_at(int c, int D) {
-  const int groups = (D + 7) >> 3;
-  return GROUPED ? ((c >> 2) & 1) * groups * 4 + (c >> 3) * 4 + (c & 3) : (c & 7) * groups + (c >> 3);
+__host__ __device__ constexpr int sum_at(int c, int D) {
+  return GROUPED ? ((c >> 2) & 1) * (D >> 1) + (c >> 3) * 4 + (c & 3) : c + (c >> 5);
+}
+template <bool GROUPED>
+__host__ __device__ constexpr int sum_len(int D) {
+  return GROUPED ? D : (D + (D >> 5) + 4) / 4 * 4;
 }
 
 template <bool GROUPED>
@@ -642,6 +649,9 @@ __device__ __forceinline__ void add_sums(float* acc, int c, int D, const float (
     b.x += v[4]; b.y += v[5]; b.z += v[6]; b.w += v[7];
     *p0 = a;
     *p1 = b;
+  } else if (c >= 0 && c + 8 <= D) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[sum_at<false>(c + j, D)] += v[j];
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -656,13 +666,13 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const BwdArgs a) 
   pdl_wait();
   pdl_trigger();
   const int t = threadIdx.x, nt = blockDim.x, D = a.D;
-  const int sum_len = (D + 7) / 8 * 8;
+  const int len = sum_len<GROUPED>(D);
   const bool sum_s = a.part_post || a.part_s || a.dgate;
   float* acc_pre = sums;                                          // sum dy n
-  float* acc_s = acc_pre + (a.part_pre ? sum_len : 0);            // sum dr nh
-  float* acc_post = acc_s + (sum_s ? sum_len : 0);                // sum gate S, when there is a gate
+  float* acc_s = acc_pre + (a.part_pre ? len : 0);            // sum dr nh
+  float* acc_post = acc_s + (sum_s ? len : 0);                    // sum gate S, when there is a gate
   {
-    const int total = ((a.part_pre ? 1 : 0) + (sum_s ? 1 : 0) + (a.part_post && a.gate ? 1 : 0)) * sum_len;
+    const int total = ((a.part_pre ? 1 : 0) + (sum_s ? 1 : 0) + (a.part_post && a.gate ? 1 : 0)) * len;
     for (int i = t; i < total; i += nt) sums[i] = 0.0f;
     __syncthreads();
   }
@@ -1096,6 +1106,256 @@ __global__ void __launch_bounds__(kBwdStreamThreads) norm_bwd_stream_kernel(cons
   }
 }
 
+// The same for a D that is no multiple of 8.  The columns of a thread's groups
+// move with the place where a row starts, which rows 8 apart share: a block takes
+// the rows of a chunk in that order (every 8th from the first, every 8th
+// from the second, ...), so that the weights in registers serve several rows.
+// The column sums are in shared memory, where any thread adds to any column, a
+// barrier between rows.
+constexpr int kRaggedThreads = 576;   // 112 registers: one block of a row of 4600 values, two of 2300
+
+template <typename XT, typename HT, typename YT, int VPT>
+__global__ void __launch_bounds__(kRaggedThreads) norm_bwd_ragged_kernel(const BwdArgs a, int stages, int groups) {
+  extern __shared__ __align__(128) uint8_t dyn[];
+  __shared__ float red[2][4 * 32];
+  __shared__ uint64_t full_bar[kMaxStages];
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
+  const int t = threadIdx.x, nt = blockDim.x, D = a.D;
+  const int len = sum_len<false>(D), span = groups * 8;       // values of a stage's tensor
+  const bool sum_s = a.part_post || a.part_s || a.dgate;
+  float* acc_p = reinterpret_cast<float*>(dyn);
+  float* acc_s = acc_p + (a.part_pre ? len : 0);
+  uint8_t* ring = reinterpret_cast<uint8_t*>(acc_s + (sum_s ? len : 0));
+  const int y_off = a.dy ? span * (int)sizeof(XT) : 0, u_off = y_off + (a.dy ? span * (int)sizeof(YT) : 0),
+            h_off = u_off + (a.dx_out ? span * (int)sizeof(XT) : 0),
+            stage_bytes = h_off + (a.load_h ? span * (int)sizeof(HT) : 0);
+  if (t == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&full_bar[s], 1);
+    abort_word = 0;
+    fence_mbar_init();
+  }
+  for (int i = t; i < (int)(reinterpret_cast<float*>(ring) - acc_p); i += nt) acc_p[i] = 0.0f;
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+
+  struct Rows {
+    int64_t chunk, row, begin, end, grp;
+  };
+  auto open = [&](Rows& r) {     // from r.chunk on, the first chunk with rows
+    for (; r.chunk < a.plan.chunks; r.chunk += gridDim.x) {
+      r.grp = r.chunk / a.plan.per_group;
+      r.begin = r.row = r.grp * a.plan.group_rows + (r.chunk % a.plan.per_group) * a.plan.chunk_rows;
+      r.end = min(min(a.M, (r.grp + 1) * a.plan.group_rows), r.begin + a.plan.chunk_rows);
+      if (r.row < r.end) return;
+    }
+  };
+  auto after = [](const Rows& r) {   // the chunk's row after r.row, or its end
+    if (r.row + 8 < r.end) return r.row + 8;
+    const int64_t next = (r.row - r.begin) % 8 + 1;
+    return next < 8 && r.begin + next < r.end ? r.begin + next : r.end;
+  };
+  auto step = [&](Rows& r) {
+    r.row = after(r);
+    if (r.row == r.end) {
+      r.chunk += gridDim.x;
+      open(r);
+    }
+  };
+  const int64_t total = a.M * D;
+  auto issue = [&](const Rows& r, int s) {
+    uint8_t* st = ring + (size_t)s * stage_bytes;
+    const int64_t g0 = r.row * D / 8, g1 = min((r.row * D + D + 7) / 8, total / 8);
+    const uint32_t n = (uint32_t)(g1 - g0) * 8;
+    mbar_arrive_expect_tx(&full_bar[s], n * (uint32_t)((a.dy ? sizeof(XT) + sizeof(YT) : 0) +
+                                                       (a.dx_out ? sizeof(XT) : 0) + (a.load_h ? sizeof(HT) : 0)));
+    if (n == 0) return;
+    if (a.dy) {
+      bulk_load(st, reinterpret_cast<const XT*>(a.x) + g0 * 8, n * (uint32_t)sizeof(XT), &full_bar[s]);
+      bulk_load(st + y_off, reinterpret_cast<const YT*>(a.dy) + g0 * 8, n * (uint32_t)sizeof(YT), &full_bar[s]);
+    }
+    if (a.dx_out) bulk_load(st + u_off, reinterpret_cast<const XT*>(a.dx_out) + g0 * 8, n * (uint32_t)sizeof(XT), &full_bar[s]);
+    if (a.load_h) bulk_load(st + h_off, reinterpret_cast<const HT*>(a.h) + g0 * 8, n * (uint32_t)sizeof(HT), &full_bar[s]);
+  };
+  Rows ahead, now;               // the next row to ask for (thread 0); the row at work
+  ahead.chunk = now.chunk = blockIdx.x;
+  open(now);
+  if (t == 0) {
+    open(ahead);
+    for (int s = 0; s < stages && ahead.chunk < a.plan.chunks; ++s) {
+      issue(ahead, s);
+      step(ahead);
+    }
+  }
+  float gw[VPT][8], wp[VPT][8];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) gw[k][j] = wp[k][j] = 0.0f;
+  int s = 0, use = 0, parity = 0, held_shift = -1;
+  int64_t held = -1;
+  bool first = true;             // no chunk of this block has added to part_post
+  float rsx = 0.0f, rsh = 1.0f, rsx_next = 0.0f, rsh_next = 1.0f;
+  auto factors = [&](int64_t m) {
+    if (a.dy) rsx_next = a.rstd_pre[m];
+    if (a.post) rsh_next = a.rstd_post[m];
+  };
+  if (now.chunk < a.plan.chunks) factors(now.row);
+  // One group of a stage's tensor, 0 outside the row; the group that the tensor
+  // ends in is read from global memory.
+  auto fetch = [&](const auto* tensor, const uint8_t* staged, int64_t flat, int g, int c, float(&v)[8]) {
+    using T = typename std::remove_const<typename std::remove_pointer<decltype(tensor)>::type>::type;
+    if (flat + c + 8 <= total) {
+      Raw8<T> raw;
+      raw.load(reinterpret_cast<const T*>(staged) + g * 8);
+      raw.to_f32(v);
+      if (c < 0 || c + 8 > D) mask8(v, c, D);
+    } else {
+      load8(tensor + flat, c, D, false, v);
+    }
+  };
+  while (now.chunk < a.plan.chunks) {
+    const int64_t m = now.row, flat = m * D;
+    const int shift = (int)(flat & 7);
+    const uint8_t* st = ring + (size_t)s * stage_bytes;
+    if (now.grp != held || shift != held_shift) {
+      held = now.grp;
+      held_shift = shift;
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int c = (t + k * nt) * 8 - shift;
+        if (c >= D) continue;
+        if (a.dh) {
+          float w[8];
+          loadw8<false>(a.w_post, a.w_f32, 0, D, c, D, a.w_post ? a.offset : 1.0f, w);
+          loadw8<false>(a.gate, a.w_f32, now.grp * D, a.gate_len, c, D, a.gate ? 0.0f : 1.0f, gw[k]);
+          mul8(gw[k], w);
+        }
+        if (a.dy) loadw8<false>(a.w_pre, a.w_f32, 0, D, c, D, a.offset, wp[k]);
+      }
+    }
+    rsx = rsx_next;
+    rsh = rsh_next;
+    const bool last_row = after(now) == now.end;
+    {
+      Rows next = now;
+      step(next);
+      if (next.chunk < a.plan.chunks) factors(next.row);
+    }
+    float n[VPT][8], u[VPT][8], nh[VPT][8], sum[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    mbar_wait(&full_bar[s], use & 1, abort_flag, 1u << 22);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int g = t + k * nt, c = g * 8 - shift;
+      if (c >= D) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) n[k][j] = u[k][j] = nh[k][j] = 0.0f;
+      if (a.dx_out) fetch(reinterpret_cast<const XT*>(a.dx_out), st + u_off, flat, g, c, u[k]);
+      if (a.dy) {
+        float dy[8], w[8];
+        fetch(reinterpret_cast<const XT*>(a.x), st, flat, g, c, n[k]);
+        fetch(reinterpret_cast<const YT*>(a.dy), st + y_off, flat, g, c, dy);
+        mul8(n[k], rsx);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = dy[j];
+        mul8(w, n[k]);
+        if (a.part_pre) add_sums<false>(acc_p, c, D, w);
+        mul8(dy, wp[k]);                                // dn
+        dot8(sum[0], sum[1], dy, n[k]);
+        fma8(u[k], rsx, dy, u[k]);
+      }
+      if (a.load_h) {
+        fetch(reinterpret_cast<const HT*>(a.h), st + h_off, flat, g, c, nh[k]);
+        mul8(nh[k], rsh);
+        if (a.post && a.dh) {
+          float q[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) q[j] = nh[k][j];
+          mul8(q, gw[k]);
+          dot8(sum[2], sum[3], u[k], q);
+          dot8(sum[4], sum[5], n[k], q);
+        }
+      }
+    }
+    float tot[3] = {sum[0] + sum[1], sum[2] + sum[3], sum[4] + sum[5]};
+    block_sums3(tot, red[parity]);        // also: every thread has read the stage and added its row to acc_p
+    parity ^= 1;
+    if (t == 0 && ahead.chunk < a.plan.chunks) {
+      issue(ahead, s);
+      step(ahead);
+    }
+    if (++s == stages) {
+      s = 0;
+      ++use;
+    }
+    const float k1 = rsx * (tot[0] * a.inv_d);
+    const float c2 = (tot[1] - k1 * tot[2]) * a.inv_d;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int c = (t + k * nt) * 8 - shift;
+      if (c >= D) continue;
+      const bool full = c >= 0 && c + 8 <= D;
+      float(&dr)[8] = u[k];
+      float o[8];
+      fma8(dr, -k1, n[k], dr);
+      if (sum_s) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = dr[j];
+        mul8(o, nh[k]);
+        add_sums<false>(acc_s, c, D, o);
+      }
+      if (a.dx) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = dr[j];
+        mul8(o, a.alpha);
+        store8(reinterpret_cast<XT*>(a.dx) + flat, c, D, full, o);
+      }
+      if (a.dh) {
+        mul8(dr, gw[k]);                 // dnh
+        if (a.post) {
+          fma8(dr, -c2, nh[k], dr);
+          mul8(dr, rsh);
+        }
+        store8(reinterpret_cast<HT*>(a.dh) + flat, c, D, full, dr);
+      }
+    }
+    if (last_row && sum_s && a.gate) {
+      __syncthreads();
+      for (int c = t; c < D; c += nt) {
+        const int i = sum_at<false>(c, D);
+        const float sv = acc_s[i];
+        acc_s[i] = 0.0f;
+        if (a.part_post) {
+          float* dst = a.part_post + (int64_t)blockIdx.x * D + c;
+          const float g = value_at(a.gate, a.w_f32, now.grp * D + c);
+          *dst = first ? g * sv : *dst + g * sv;
+        }
+        if (a.part_s)
+          a.part_s[now.chunk * D + c] = sv;
+        else if (a.dgate)
+          a.dgate[now.grp * D + c] = sv * (a.w_post ? a.offset + value_at(a.w_post, a.w_f32, c) : 1.0f);
+      }
+      first = false;
+      __syncthreads();
+    }
+    step(now);
+  }
+  __syncthreads();
+  // chunks without rows (behind a gate's last, shorter chunk) have no part but zero
+  if (a.part_s)
+    for (int64_t chunk = blockIdx.x; chunk < a.plan.chunks; chunk += gridDim.x) {
+      const int64_t grp = chunk / a.plan.per_group, begin = grp * a.plan.group_rows + (chunk % a.plan.per_group) * a.plan.chunk_rows;
+      if (begin < min(a.M, (grp + 1) * a.plan.group_rows)) continue;
+      for (int c = t; c < D; c += nt) a.part_s[chunk * D + c] = 0.0f;
+    }
+  for (int c = t; c < D; c += nt) {
+    const int i = sum_at<false>(c, D);
+    if (a.part_pre) a.part_pre[(int64_t)blockIdx.x * D + c] = acc_p[i];
+    if (a.part_post && (!a.gate || first)) a.part_post[(int64_t)blockIdx.x * D + c] = a.gate ? 0.0f : acc_s[i];
+  }
+}
+
 // Adds the parts in a fixed order: 32 columns per block, every warp takes each
 // 32nd part.  blockIdx.y 0: dw_pre; 1: dw_post, from its parts or from those of
 // S (a few gates); 2 + g: dgate's row g.
@@ -1117,9 +1377,6 @@ struct FinishArgs {
   bool w_f32;
 };
 
-__device__ __forceinline__ float value_at(const void* p, bool f32, int64_t i) {
-  return f32 ? reinterpret_cast<const float*>(p)[i] : to_f32(reinterpret_cast<const bf16*>(p)[i]);
-}
 
 // The sum over `parts` rows of src at this block's column `lane`, in warp 0.
 __device__ __forceinline__ float sum_parts(const float* src, int64_t parts, int c, int D, float (*buf)[33]) {
@@ -1177,12 +1434,13 @@ int groups_per_thread(int64_t D) {
 }
 unsigned row_threads(int64_t D, int vpt) { return (unsigned)((row_groups(D) + vpt * 32 - 1) / (vpt * 32) * 32); }
 
-int bwd_stream_vpt(int64_t D) { return D <= 8 * kBwdStreamThreads ? 1 : 2; }
+int bwd_stream_threads(int64_t D) { return D % 8 ? kRaggedThreads : kBwdStreamThreads; }
+int bwd_stream_vpt(int64_t D) { return row_groups(D) <= bwd_stream_threads(D) ? 1 : 2; }
 
-// Rows that fit two groups per thread and are more than the SMs take one of each.
+// Rows that fit two groups per thread and are more than the SMs are streamed.
 bool bwd_streams(int64_t M, int64_t D) {
   const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
-  return D % 8 == 0 && D >= 512 && D <= 2 * 8 * kBwdStreamThreads && M > sms;
+  return D >= 512 && row_groups(D) <= 2 * bwd_stream_threads(D) && D <= 8192 && M > sms;
 }
 
 BwdPlan bwd_plan(int64_t M, int64_t D, int64_t gate_rows) {
@@ -1191,7 +1449,7 @@ BwdPlan bwd_plan(int64_t M, int64_t D, int64_t gate_rows) {
   p.groups = (M + p.group_rows - 1) / p.group_rows;
   const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
   // blocks that an SM holds: of norm_bwd_stream_kernel at 128 registers, or of norm_bwd_kernel
-  const int per_sm = bwd_streams(M, D) ? std::max(1, kBwdStreamThreads / (int)row_threads(D, bwd_stream_vpt(D)))
+  const int per_sm = bwd_streams(M, D) ? std::max(1, bwd_stream_threads(D) / (int)row_threads(D, bwd_stream_vpt(D)))
                                        : std::max(1, std::min(8, 640 / (int)row_threads(D, groups_per_thread(D))));
   const int64_t want = std::min<int64_t>(M, (int64_t)sms * per_sm);
   // Chunks per gate: the count whose slowest block has the fewest rows to go
@@ -1271,7 +1529,8 @@ template <typename XT, typename HT, typename YT, int VPT, bool GROUPED>
 ql_status run_bwd(const BwdArgs& a, size_t smem, cudaStream_t st) {
   const auto kernel = norm_bwd_kernel<XT, HT, YT, VPT, GROUPED>;
   if (per_device(reinterpret_cast<const void*>(kernel), 0, [kernel] {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * 4 * kMaxD) != cudaSuccess) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 3 * 4 * sum_len<false>(kMaxD)) != cudaSuccess) {
           cudaGetLastError();
           return -1;
         }
@@ -1310,8 +1569,35 @@ ql_status run_bwd_stream(const BwdArgs& a, cudaStream_t st) {
   return QL_OK;
 }
 
+template <typename XT, typename HT, typename YT, int VPT>
+ql_status run_bwd_ragged(const BwdArgs& a, cudaStream_t st) {
+  const auto kernel = norm_bwd_ragged_kernel<XT, HT, YT, VPT>;
+  constexpr int kMost = 220 * 1024;
+  if (per_device(reinterpret_cast<const void*>(kernel), 0, [kernel] {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess) {
+          cudaGetLastError();
+          return -1;
+        }
+        return 1;
+      }) < 0)
+    return QL_ERR_CUDA;
+  const int groups = row_groups(a.D), threads = (int)row_threads(a.D, VPT);
+  const int row = groups * 8 * ((a.dy ? (int)(sizeof(XT) + sizeof(YT)) : 0) + (a.dx_out ? (int)sizeof(XT) : 0) +
+                                (a.load_h ? (int)sizeof(HT) : 0));
+  const int fixed = sum_len<false>(a.D) * 4 * ((a.part_pre ? 1 : 0) + (a.part_post || a.part_s || a.dgate ? 1 : 0));
+  const int share = kMost / std::max(1, kRaggedThreads / threads) - 2048;
+  const int stages = std::max(1, std::min(kMaxStages, (share - fixed) / row));
+  TraceScope ts(TK_NORM, st);
+  QL_CUDA_TRY(launch(kernel, dim3((unsigned)a.plan.blocks), dim3((unsigned)threads), (size_t)fixed + (size_t)stages * row,
+                     st, 1, 1, a, stages, groups));
+  QL_LAUNCH_CHECK();
+  return QL_OK;
+}
+
 template <typename XT, typename HT, typename YT, bool GROUPED>
 ql_status pick_bwd(const BwdArgs& a, size_t smem, cudaStream_t st) {
+  if (!GROUPED && bwd_streams(a.M, a.D))
+    return bwd_stream_vpt(a.D) == 1 ? run_bwd_ragged<XT, HT, YT, 1>(a, st) : run_bwd_ragged<XT, HT, YT, 2>(a, st);
   if (GROUPED && bwd_streams(a.M, a.D)) {
     const bool sums = a.part_pre || a.part_post || a.part_s || a.dgate;
     if (bwd_stream_vpt(a.D) == 1)
@@ -1415,7 +1701,7 @@ ql_status launch_block_norm_bwd(const ql_block_norm* n, const void* x_out, ql_dt
   a.w_f32 = n->w_dt == QL_F32;
   a.post = h && n->w_post;
   a.load_h = (dh && a.post) || dw_post || dgate;
-  const int64_t len = (D + 7) / 8 * 8;
+  const int len = D % 8 ? sum_len<false>((int)D) : sum_len<true>((int)D);
   const size_t smem = (size_t)len * 4 * ((dw_pre ? 1 : 0) + (dw_post || dgate ? 1 : 0) + (a.part_post && n->gate ? 1 : 0));
   const bool yf = dy && dy_dt == QL_F32;
   ql_status rc;

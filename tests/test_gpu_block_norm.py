@@ -147,11 +147,13 @@ def test_gates(q, gate_rows, post, D):
 
 def test_many_rows(q):
     """More rows than the blocks take at once, in several chunks per gate."""
-    for gate_rows in (0, 700, 5000):
-        c = Case(q, 5000, 264, gate_rows=gate_rows)
-        c.forward(q)
-        c.check_forward()
-        c.check_backward(c.backward(q))
+    for D, M in ((264, 5000), (1032, 1700), (1029, 1700), (4104, 700), (4101, 700), (8191, 300)):
+        for gate_rows in (0, 1, 3, 333, M):
+            c = Case(q, M, D, gate_rows=gate_rows, yt=F32 if D % 2 else BF)
+            c.forward(q)
+            c.check_forward(f"{M}x{D}/{gate_rows}")
+            c.check_backward(c.backward(q), what=f"{M}x{D}/{gate_rows}")
+            c.check_backward(c.backward(q, sums=False, dx_out=False), dx_out=False, what=f"{M}x{D}/{gate_rows} frozen")
 
 
 @pytest.mark.parametrize("D", [96, 99, 2048, 2049])
