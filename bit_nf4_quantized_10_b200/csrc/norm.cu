@@ -677,6 +677,9 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const BwdArgs a) 
     __syncthreads();
   }
   int parity = 0;
+  // Up to two groups stay in registers between the sums and the results; of more
+  // (D > 8192) each is read again, from L2 (four kept spilled: 1000 x 16384 took 257 us).
+  constexpr int KEPT = VPT <= 2 ? VPT : 1;
   for (int64_t chunk = blockIdx.x; chunk < a.plan.chunks; chunk += gridDim.x) {
     const int64_t grp = chunk / a.plan.per_group;
     const int64_t group_end = min(a.M, (grp + 1) * a.plan.group_rows);
@@ -686,91 +689,91 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const BwdArgs a) 
     for (int64_t m = row0; m < row1; ++m) {
       const int64_t flat = m * D;
       const int shift = GROUPED ? 0 : (int)(flat & 7);
-      float n[VPT][8], u[VPT][8], nh[VPT][8], gw[VPT][8];
+      float n[KEPT][8], u[KEPT][8], nh[KEPT][8], gw[KEPT][8];
       const float rsx = a.dy ? a.rstd_pre[m] : 0.0f;
       const float rsh = a.post ? a.rstd_post[m] : 1.0f;
       float s[3] = {0.0f, 0.0f, 0.0f};   // sum dn n, sum u q, sum n q  with q = gate (o + w_post) nh
+      // One group of the row: n, u = dx' + rsx dn, nh and gate (o + w_post); the
+      // first time also its share of the sums.
+      auto group = [&](int c, bool full, bool sums, float(&n)[8], float(&u)[8], float(&nh)[8], float(&gw)[8]) {
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int c = (t + v * nt) * 8 - shift;
-        const bool full = GROUPED || (c >= 0 && c + 8 <= D);
-        if (c >= D) continue;
+        for (int j = 0; j < 8; ++j) n[j] = u[j] = nh[j] = gw[j] = 0.0f;
         float dy[8];
         if (a.dy) {
-          load8(reinterpret_cast<const XT*>(a.x) + flat, c, D, full, n[v]);
+          load8(reinterpret_cast<const XT*>(a.x) + flat, c, D, full, n);
           load8(reinterpret_cast<const YT*>(a.dy) + flat, c, D, full, dy);
         }
-        if (a.dx_out) load8(reinterpret_cast<const XT*>(a.dx_out) + flat, c, D, full, u[v]);
-        else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) u[v][j] = 0.0f;
-        }
-        if (a.load_h) load8(reinterpret_cast<const HT*>(a.h) + flat, c, D, full, nh[v]);
-        else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) nh[v][j] = 0.0f;
+        if (a.dx_out) load8(reinterpret_cast<const XT*>(a.dx_out) + flat, c, D, full, u);
+        if (a.load_h) {
+          load8(reinterpret_cast<const HT*>(a.h) + flat, c, D, full, nh);
+          mul8(nh, rsh);
         }
         float w[8];
         if (a.dh) {
           loadw8<GROUPED>(a.w_post, a.w_f32, 0, D, c, D, a.w_post ? a.offset : 1.0f, w);
-          loadw8<GROUPED>(a.gate, a.w_f32, grow, a.gate_len, c, D, a.gate ? 0.0f : 1.0f, gw[v]);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) gw[v][j] *= w[j];
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) gw[v][j] = 0.0f;
+          loadw8<GROUPED>(a.gate, a.w_f32, grow, a.gate_len, c, D, a.gate ? 0.0f : 1.0f, gw);
+          mul8(gw, w);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) nh[v][j] *= rsh;
         if (a.dy) {
           loadw8<GROUPED>(a.w_pre, a.w_f32, 0, D, c, D, a.offset, w);
-          float dyn[8];
+          mul8(n, rsx);
+          if (sums && a.part_pre) {
+            float dyn[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            n[v][j] *= rsx;
-            dyn[j] = dy[j] * n[v][j];
-            const float dn = dy[j] * w[j];
-            u[v][j] += rsx * dn;
-            s[0] += dn * n[v][j];
+            for (int j = 0; j < 8; ++j) dyn[j] = dy[j] * n[j];
+            add_sums<GROUPED>(acc_pre, c, D, dyn);
           }
-          if (a.part_pre) add_sums<GROUPED>(acc_pre, c, D, dyn);
-        } else {
+          mul8(dy, w);                   // dn
+          fma8(u, rsx, dy, u);
+          if (sums) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) n[v][j] = 0.0f;
-        }
-        if (a.post) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float qv = gw[v][j] * nh[v][j];
-            s[1] += u[v][j] * qv;
-            s[2] += n[v][j] * qv;
+            for (int j = 0; j < 8; ++j) s[0] += dy[j] * n[j];
           }
         }
+        if (sums && a.post) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float qv = gw[j] * nh[j];
+            s[1] += u[j] * qv;
+            s[2] += n[j] * qv;
+          }
+        }
+      };
+#pragma unroll(VPT == KEPT ? VPT : 1)
+      for (int v = 0; v < VPT; ++v) {
+        const int c = (t + v * nt) * 8 - shift;
+        const int at = VPT == KEPT ? v : 0;
+        if (c < D) group(c, GROUPED || (c >= 0 && c + 8 <= D), true, n[at], u[at], nh[at], gw[at]);
       }
       // dr = u - rsx c1 n with c1 = mean(dn n), so mean(dnh nh) = mean(u q) - rsx c1 mean(n q)
       block_sums3(s, red[parity]);
       parity ^= 1;
       const float k1 = rsx * (s[0] * a.inv_d);
       const float c2 = (s[1] - k1 * s[2]) * a.inv_d;
-#pragma unroll
+#pragma unroll(VPT == KEPT ? VPT : 1)
       for (int v = 0; v < VPT; ++v) {
         const int c = (t + v * nt) * 8 - shift;
         const bool full = GROUPED || (c >= 0 && c + 8 <= D);
         if (c >= D) continue;
-        float o[8], sv[8];
+        const int at = VPT == KEPT ? v : 0;
+        if (VPT != KEPT) group(c, full, false, n[0], u[0], nh[0], gw[0]);
+        float o[8];
+        fma8(u[at], -k1, n[at], u[at]);      // dr
+        if (sum_s) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          u[v][j] -= k1 * n[v][j];       // dr
-          o[j] = a.alpha * u[v][j];
-          sv[j] = u[v][j] * nh[v][j];
+          for (int j = 0; j < 8; ++j) o[j] = u[at][j] * nh[at][j];
+          add_sums<GROUPED>(acc_s, c, D, o);
         }
-        if (a.dx) store8(reinterpret_cast<XT*>(a.dx) + flat, c, D, full, o);
-        if (sum_s) add_sums<GROUPED>(acc_s, c, D, sv);
+        if (a.dx) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] = a.alpha * u[at][j];
+          store8(reinterpret_cast<XT*>(a.dx) + flat, c, D, full, o);
+        }
         if (a.dh) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            o[j] = u[v][j] * gw[v][j];
-            if (a.post) o[j] = rsh * (o[j] - nh[v][j] * c2);
+            o[j] = u[at][j] * gw[at][j];
+            if (a.post) o[j] = rsh * (o[j] - nh[at][j] * c2);
           }
           store8(reinterpret_cast<HT*>(a.dh) + flat, c, D, full, o);
         }
@@ -1440,7 +1443,7 @@ int bwd_stream_vpt(int64_t D) { return row_groups(D) <= bwd_stream_threads(D) ? 
 // Rows that fit two groups per thread and are more than the SMs are streamed.
 bool bwd_streams(int64_t M, int64_t D) {
   const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
-  return D >= 512 && row_groups(D) <= 2 * bwd_stream_threads(D) && D <= 8192 && M > sms;
+  return D >= 64 && row_groups(D) <= 2 * bwd_stream_threads(D) && D <= 8192 && M > sms;
 }
 
 BwdPlan bwd_plan(int64_t M, int64_t D, int64_t gate_rows) {
