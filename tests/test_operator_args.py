@@ -118,10 +118,10 @@ def test_int8(lib):
     assert g(K=40) == no and g(K=131072) == no and g(M=1 << 31) == no and g(N=1 << 31) == no
     assert g(M=(1 << 31) - 1, N=(1 << 31) - 1) == no
     assert g(M=0) == lib.QL_OK
-    need = lib.qlora_workspace_size(lib.QL_OP_INT8_GEMM, 8, 28672, 8192)
-    assert need > 0
-    assert g(M=8, N=28672, K=8192, wb=need - 1) == lib.QL_ERR_WORKSPACE
-    assert g(M=8, N=28672, K=8192, ws=FAKE + 4, wb=need) == bad
+    need = lib.qlora_workspace_size(lib.QL_OP_INT8_GEMM, 33, 1024, 28672)      # split along K
+    assert need > 0 and lib.qlora_workspace_size(lib.QL_OP_INT8_GEMM, 8, 28672, 8192) == 0
+    assert g(M=33, N=1024, K=28672, wb=need - 1) == lib.QL_ERR_WORKSPACE
+    assert g(M=33, N=1024, K=28672, ws=FAKE + 4, wb=need) == bad
 
 
 def test_binding_refuses_what_the_library_cannot_see(lib):
