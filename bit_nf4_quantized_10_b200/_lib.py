@@ -440,6 +440,8 @@ def qlora_block_norm_bwd(norm: BlockNorm, x_out, h, rstd_pre, rstd_post, dx_out,
                          dgate=None, ws=None, stream=None) -> None:
     """Gradients of qlora_block_norm_fwd: dx [M, D] and dh [M, D] from dx_out and dy (either may be None), and the
     fp32 sums dw_pre [D], dw_post [D] and dgate [G, D] where given (they need the workspace)."""
+    if dy is None and dx_out is None:
+        raise ValueError("dx_out or dy must be given")
     M, D = shape = (dy if dy is not None else dx_out).shape
     dev, rows = _device(), (M,)
     xs = x_out if x_out is not None else dx_out if dx_out is not None else dx

@@ -460,8 +460,8 @@ ql_status qlora_block_norm_fwd(const ql_block_norm* norm, const void* x, ql_dtyp
   ql_status st = check_norm(norm, M, D, h != nullptr);
   if (st != QL_OK) return st;
   if (!dtype_ok(x_dt) || (h && !dtype_ok(h_dt)) || (y && !dtype_ok(y_dt))) return QL_ERR_INVALID_ARG;
-  if ((!x_out && !y) || (y && !norm->w_pre)) return QL_ERR_INVALID_ARG;
   if (M == 0) return QL_OK;
+  if ((!x_out && !y) || (y && !norm->w_pre)) return QL_ERR_INVALID_ARG;
   if (!aligned16(x) || !opt16(h) || !opt16(x_out) || !opt16(y) || !opt16(rstd_pre) || !opt16(rstd_post))
     return QL_ERR_INVALID_ARG;
   return ql::launch_block_norm_fwd(norm, x, x_dt, h, h ? h_dt : x_dt, M, D, x_out, y, y_dt, rstd_pre, rstd_post,
@@ -478,7 +478,6 @@ ql_status qlora_block_norm_bwd(const ql_block_norm* norm, const void* x_out, ql_
   ql_status st = check_norm(norm, M, D, branch);
   if (st != QL_OK) return st;
   if (!dtype_ok(x_dt) || (branch && !dtype_ok(h_dt)) || (dy && !dtype_ok(dy_dt))) return QL_ERR_INVALID_ARG;
-  if (!dx && !dh && !dw_pre && !dw_post && !dgate) return QL_ERR_INVALID_ARG;
   if ((dw_pre && !aligned16(dw_pre)) || (dw_post && !aligned16(dw_post)) || (dgate && !aligned16(dgate)))
     return QL_ERR_INVALID_ARG;
   if (dgate && !norm->gate) return QL_ERR_INVALID_ARG;
@@ -489,6 +488,7 @@ ql_status qlora_block_norm_bwd(const ql_block_norm* norm, const void* x_out, ql_
     if (dw_post) QL_CUDA_TRY(cudaMemsetAsync(dw_post, 0, (size_t)D * 4, cs));
     return QL_OK;
   }
+  if (!dx && !dh && !dw_pre && !dw_post && !dgate) return QL_ERR_INVALID_ARG;
   if (!dx_out && !dy) return QL_ERR_INVALID_ARG;
   if (dy && (!norm->w_pre || !aligned16(dy) || !aligned16(x_out) || !aligned16(rstd_pre))) return QL_ERR_INVALID_ARG;
   if (dw_pre && !dy) return QL_ERR_INVALID_ARG;

@@ -452,7 +452,7 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-template <typename XT, typename HT, typename WT, bool GROUPED>
+template <typename XT, typename HT, typename WT, bool GROUPED, bool HAS_H>
 __global__ void __launch_bounds__(kStreamThreads) norm_fwd_stream_kernel(const FwdArgs a, int stages, int groups) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float red[3][32];
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kStreamThreads) norm_fwd_stream_kernel(const F
   volatile int* abort_flag = &abort_word;
   constexpr int VPT = kStreamVpt;
   const int t = threadIdx.x, nt = blockDim.x, D = a.D;
-  const int x_bytes = groups * 8 * (int)sizeof(XT), stage_bytes = groups * 8 * (int)(sizeof(XT) + sizeof(HT));
+  const int x_bytes = groups * 8 * (int)sizeof(XT), stage_bytes = x_bytes + (HAS_H ? groups * 8 * (int)sizeof(HT) : 0);
   if (t == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&full_bar[s], 1);
     abort_word = 0;
@@ -478,10 +478,10 @@ __global__ void __launch_bounds__(kStreamThreads) norm_fwd_stream_kernel(const F
     const int64_t g0 = m * D / 8, g1 = GROUPED ? (m + 1) * D / 8 : min(((m + 1) * D + 7) / 8, total / 8);
     uint8_t* st = ring + (size_t)s * stage_bytes;
     const uint32_t n = (uint32_t)(g1 - g0) * 8;
-    mbar_arrive_expect_tx(&full_bar[s], n * (uint32_t)(sizeof(XT) + sizeof(HT)));
+    mbar_arrive_expect_tx(&full_bar[s], n * (uint32_t)(sizeof(XT) + (HAS_H ? sizeof(HT) : 0)));
     if (n) {
       bulk_load(st, reinterpret_cast<const XT*>(a.x) + g0 * 8, n * (uint32_t)sizeof(XT), &full_bar[s]);
-      bulk_load(st + x_bytes, reinterpret_cast<const HT*>(a.h) + g0 * 8, n * (uint32_t)sizeof(HT), &full_bar[s]);
+      if (HAS_H) bulk_load(st + x_bytes, reinterpret_cast<const HT*>(a.h) + g0 * 8, n * (uint32_t)sizeof(HT), &full_bar[s]);
     }
   };
   if (t == 0)
@@ -502,35 +502,36 @@ __global__ void __launch_bounds__(kStreamThreads) norm_fwd_stream_kernel(const F
     const HT* hs = reinterpret_cast<const HT*>(ring + (size_t)s * stage_bytes + x_bytes);
     mbar_wait(&full_bar[s], use & 1, abort_flag, 1u << 22);
     float v[VPT][8];
-    float s0 = 0.0f, s1 = 0.0f;
+    float s0 = 0.0f, s1 = 0.0f, rs = 1.0f;
+    if (HAS_H) {
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      const int g = t + k * nt, c = g * 8 - shift;
-      if (c >= D) continue;
-      if (GROUPED || flat + c + 8 <= total) {
-        Raw8<HT> raw;
-        raw.load(hs + g * 8);
-        raw.to_f32(v[k]);
-      } else {
-        load8(reinterpret_cast<const HT*>(a.h) + flat, c, D, false, v[k]);
+      for (int k = 0; k < VPT; ++k) {
+        const int g = t + k * nt, c = g * 8 - shift;
+        if (c >= D) continue;
+        if (GROUPED || flat + c + 8 <= total) {
+          Raw8<HT> raw;
+          raw.load(hs + g * 8);
+          raw.to_f32(v[k]);
+        } else {
+          load8(reinterpret_cast<const HT*>(a.h) + flat, c, D, false, v[k]);
+        }
+        if (!GROUPED && (c < 0 || c + 8 > D)) mask8(v[k], c, D);
+        dot8(s0, s1, v[k], v[k]);
+        if (fresh) {
+          float w[8];
+          loadw8<GROUPED>(a.w_post, sizeof(WT) == 4, 0, D, c, D, a.w_post ? a.offset : 1.0f, w);
+          loadw8<GROUPED>(a.gate, sizeof(WT) == 4, (int64_t)grow * D, a.gate_len, c, D, a.gate ? 0.0f : 1.0f, gw[k]);
+          mul8(gw[k], w);
+        }
       }
-      if (!GROUPED && (c < 0 || c + 8 > D)) mask8(v[k], c, D);
-      dot8(s0, s1, v[k], v[k]);
-      if (fresh) {
-        float w[8];
-        loadw8<GROUPED>(a.w_post, sizeof(WT) == 4, 0, D, c, D, a.w_post ? a.offset : 1.0f, w);
-        loadw8<GROUPED>(a.gate, sizeof(WT) == 4, (int64_t)grow * D, a.gate_len, c, D, a.gate ? 0.0f : 1.0f, gw[k]);
-        mul8(gw[k], w);
+      if (a.w_post) {
+        float sum[1] = {s0 + s1};
+        block_sums(sum, red[2]);
+        rs = rsqrtf(sum[0] * a.inv_d + a.eps);
+        if (t == 0 && a.rstd_post) a.rstd_post[m] = rs;
       }
+      s0 = s1 = 0.0f;
     }
-    float rs = 1.0f;
-    if (a.w_post) {
-      float sum[1] = {s0 + s1};
-      block_sums(sum, red[2]);
-      rs = rsqrtf(sum[0] * a.inv_d + a.eps);
-      if (t == 0 && a.rstd_post) a.rstd_post[m] = rs;
-    }
-    s0 = s1 = 0.0f;
     Raw8<WT> pre[VPT];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
@@ -544,9 +545,15 @@ __global__ void __launch_bounds__(kStreamThreads) norm_fwd_stream_kernel(const F
       } else {
         load8(reinterpret_cast<const XT*>(a.x) + flat, c, D, false, xv);
       }
-      mul8(v[k], rs);
-      mul8(v[k], gw[k]);
-      fma8(v[k], a.alpha, xv, v[k]);
+      if (HAS_H) {
+        mul8(v[k], rs);
+        mul8(v[k], gw[k]);
+        fma8(v[k], a.alpha, xv, v[k]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[k][j] = xv[j];
+        mul8(v[k], a.alpha);
+      }
       if (!GROUPED && (c < 0 || c + 8 > D)) mask8(v[k], c, D);
       round8(v[k], (XT*)nullptr);
       dot8(s0, s1, v[k], v[k]);
@@ -1485,9 +1492,9 @@ ql_status run_fwd(const FwdArgs& a, cudaStream_t st) {
   return QL_OK;
 }
 
-template <typename XT, typename HT, typename WT, bool GROUPED>
+template <typename XT, typename HT, typename WT, bool GROUPED, bool HAS_H>
 ql_status run_stream(const FwdArgs& a, cudaStream_t st) {
-  const auto kernel = norm_fwd_stream_kernel<XT, HT, WT, GROUPED>;
+  const auto kernel = norm_fwd_stream_kernel<XT, HT, WT, GROUPED, HAS_H>;
   constexpr int kMost = 200 * 1024;
   if (per_device(reinterpret_cast<const void*>(kernel), 0, [kernel] {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess) {
@@ -1499,7 +1506,7 @@ ql_status run_stream(const FwdArgs& a, cudaStream_t st) {
     return QL_ERR_CUDA;
   const int groups = row_groups(a.D);
   const unsigned threads = row_threads(a.D, kStreamVpt);
-  const int stage = groups * 8 * (int)(sizeof(XT) + sizeof(HT));
+  const int stage = groups * 8 * (int)(sizeof(XT) + (HAS_H ? sizeof(HT) : 0));
   // as many blocks as 1024 threads an SM allow, if two rows each fit; then as many rows as fit
   int per_sm = std::max(1, kStreamThreads / (int)threads);
   while (per_sm > 1 && per_sm * (2 * stage + 2048) > kMost) --per_sm;
@@ -1517,8 +1524,9 @@ template <typename XT, typename HT, bool GROUPED>
 ql_status pick_fwd(const FwdArgs& a, cudaStream_t st) {
   const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
   const int groups = row_groups(a.D);
-  if (a.h && groups > 128 && groups <= kStreamVpt * kStreamThreads && a.M > sms)
-    return a.w_f32 ? run_stream<XT, HT, float, GROUPED>(a, st) : run_stream<XT, HT, bf16, GROUPED>(a, st);
+  if (groups > 128 && groups <= kStreamVpt * kStreamThreads && a.M > sms)
+    return a.h ? a.w_f32 ? run_stream<XT, HT, float, GROUPED, true>(a, st) : run_stream<XT, HT, bf16, GROUPED, true>(a, st)
+           : a.w_f32 ? run_stream<XT, XT, float, GROUPED, false>(a, st) : run_stream<XT, XT, bf16, GROUPED, false>(a, st);
   // rows of up to 128 groups: one warp each, no block barrier
   if (row_groups(a.D) <= 128) return run_fwd<XT, HT, 4, GROUPED, true>(a, st);
   switch (groups_per_thread(a.D)) {
@@ -1562,9 +1570,10 @@ ql_status run_bwd_stream(const BwdArgs& a, cudaStream_t st) {
   const int row = a.D * ((a.dy ? (int)(sizeof(XT) + sizeof(YT)) : 0) + (a.dx_out ? (int)sizeof(XT) : 0) +
                          (a.load_h ? (int)sizeof(HT) : 0));
   const int fixed = VPT == 2 && a.part_pre ? a.D * 4 : 0;
-  // rows under way: as many as fit beside the other blocks of an SM, at least one
+  // rows under way: as many as fit beside the other blocks of an SM, at least
+  // those that the kernel takes at a time (two rows of 4096 are 128 KB at most)
   const int share = kMost / std::max(1, kBwdStreamThreads / threads) - 2048;
-  const int stages = std::max(1, std::min(kMaxStages, (share - fixed) / row));
+  const int stages = std::max(VPT == 1 ? 2 : 1, std::min(kMaxStages, (share - fixed) / row));
   TraceScope ts(TK_NORM, st);
   QL_CUDA_TRY(launch(kernel, dim3((unsigned)a.plan.blocks), dim3((unsigned)threads), (size_t)fixed + (size_t)stages * row,
                      st, 1, 1, a, stages));
@@ -1651,7 +1660,7 @@ ql_status launch_block_norm_fwd(const ql_block_norm* n, const void* x, ql_dtype 
   a.gate = n->gate;
   a.M = (int)M;
   a.gate_rows = (int)std::min<int64_t>(n->gate_rows, M);
-  a.gate_len = n->gate ? (M + n->gate_rows - 1) / n->gate_rows * D : 0;
+  a.gate_len = n->gate ? ((M - 1) / n->gate_rows + 1) * D : 0;
   a.D = (int)D;
   a.alpha = n->alpha;
   a.eps = n->eps;

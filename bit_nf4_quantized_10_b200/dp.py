@@ -58,7 +58,7 @@ class GradBucket:
         bits.  The padding between the views is zero and stays out of the norm.
         The tensors are the bucket's own and are overwritten by the next call."""
         from . import _lib as L
-        if not hasattr(self, "_list"):
+        if getattr(self, "_list", None) is None or self._list.tensors[0] is not self.buffer:
             self._list = L.TensorList([self.buffer])
             self._norm = torch.empty(2, 4, dtype=torch.float32, device=self.buffer.device)   # 16 bytes each
             need = L.qlora_workspace_size(L.QL_OP_GRAD_NORM, 1)

@@ -139,6 +139,8 @@ class QLoRAMLPStack:
         dx, dy = dx_out, dy_out
         for i in reversed(range(len(self.mlps))):
             j = i + 1
+            if dy is None and self.dw_pre[j] is not None:
+                self.dw_pre[j].zero_()
             q.qlora_block_norm_bwd(self.norms[j], self.x[j], self.h[i], self.rstd_pre[j], self.rstd_post[j], dx, dy,
                                    self.dx, self.dh, dw_pre=self.dw_pre[j] if dy is not None else None,
                                    dw_post=self.dw_post[j], dgate=self.dgate[j], ws=self.ws)

@@ -464,7 +464,8 @@ ql_status qlora_adamw_step_clipped(float* p, const float* g, float* m, float* v,
  *   NULL (x' = round(alpha x); w_post and gate are then unused); x_out device
  *   out [M, D] of x_dt or NULL; y device out [M, D] of y_dt or NULL (no norm;
  *   w_pre is then unused, and required otherwise).  rstd_pre, rstd_post device
- *   out fp32 [M] or NULL: what the backward pass needs.  x_out may be x.
+ *   out fp32 [M] or NULL: what the backward pass needs (written where y is, and
+ *   where h and w_post are given).  x_out may be x.
  *   Neither x_out nor y may otherwise overlap another argument.
  * qlora_block_norm_bwd: gradients of <dx_out, x'> + <dy, y> for the call above:
  *   x_out device [M, D] of x_dt: x' as stored (only read when dy is given);

@@ -157,8 +157,9 @@ def test_many_rows(q):
 
 
 @pytest.mark.parametrize("D", [96, 99, 2048, 2049])
-def test_parts_left_out(q, D):
-    c = Case(q, 21, D, gate_rows=6)
+@pytest.mark.parametrize("M", [21, 300])
+def test_parts_left_out(q, M, D):
+    c = Case(q, M, D, gate_rows=6)
     c.forward(q)
     for dx_out, dy in ((True, False), (False, True)):
         c.check_backward(c.backward(q, dx_out=dx_out, dy=dy), dx_out, dy)
@@ -167,10 +168,20 @@ def test_parts_left_out(q, D):
     for name in ("dx", "dh"):
         assert torch.equal(frozen[name], trained[name])
     # the norm in front of the first block: no block output
-    n = Case(q, 21, D, h=False, post=False)
+    n = Case(q, M, D, h=False, post=False)
     n.forward(q)
     n.check_forward()
     n.check_backward(n.backward(q))
+    # sums alone, and the stream's gradient alone
+    o = {"dw_pre": torch.empty(D, device="cuda"), "dw_post": torch.empty(D, device="cuda"),
+         "dgate": torch.empty(c.gate.shape, device="cuda")}
+    ws = torch.empty(q.qlora_workspace_size(q.QL_OP_BLOCK_NORM_BWD, M, D, 6), dtype=torch.uint8, device="cuda")
+    q.qlora_block_norm_bwd(c.norm, c.x_out, c.h, c.rstd_pre, c.rstd_post, c.dx_out, c.dy, None, None, ws=ws, **o)
+    for name in o:
+        assert torch.equal(o[name], trained[name]), name
+    dx = torch.empty_like(c.x)
+    q.qlora_block_norm_bwd(c.norm, c.x_out, None, c.rstd_pre, None, c.dx_out, c.dy, dx, None)
+    assert torch.equal(dx, trained["dx"])
     # after the last block: the stream alone
     x_only = torch.empty_like(c.x)
     q.qlora_block_norm_fwd(c.norm, c.x, c.h, x_only, None)
@@ -211,6 +222,34 @@ def test_in_place_and_neighbours_untouched(q, D):
     assert torch.equal(g, o["dx"]) and torch.equal(dh, o["dh"])
     for b in (xb, yb, gb, hb):
         assert bool((b[M * D:] == 7.0).all())
+
+
+def test_a_gate_for_more_rows_than_there_are(q):
+    """gate_rows far past M (and past 32 bits) is one gate for all."""
+    c = Case(q, 30, 264, gate_rows=30)
+    c.forward(q)
+    want = c.x_out.clone()
+    c.norm = q.BlockNorm(c.w_pre, c.w_post, c.gate, 2 ** 62)
+    c.forward(q)
+    assert torch.equal(c.x_out, want)
+    assert torch.equal(c.backward(q)["dgate"], Case.backward(c, q)["dgate"])
+
+
+def test_no_gradient_at_all_is_refused(q):
+    c = Case(q, 3, 64)
+    with pytest.raises(ValueError):
+        q.qlora_block_norm_bwd(c.norm, c.x_out, c.h, c.rstd_pre, c.rstd_post, None, None, c.x, None)
+
+
+@pytest.mark.parametrize("D", [1024, 1025])
+def test_no_tokens(q, D):
+    c = Case(q, 2, D)
+    e = lambda t: t[:0]  # noqa: E731
+    q.qlora_block_norm_fwd(c.norm, e(c.x), e(c.h), e(c.x_out), e(c.y), e(c.rstd_pre), e(c.rstd_post))
+    dw = torch.ones(D, device="cuda")
+    q.qlora_block_norm_bwd(c.norm, e(c.x), e(c.h), e(c.rstd_pre), e(c.rstd_post), e(c.dx_out), e(c.dy), e(c.x_out),
+                           e(c.h), dw_pre=dw)
+    assert not dw.any()
 
 
 def test_rows_of_zeros_and_non_finite_rows(q):
