@@ -49,24 +49,71 @@ bool make_map_2d(CUtensorMap* map, CUtensorMapDataType dt, int elem_bytes, const
 namespace i8 {
 
 // ------------------------------------------------------------------ quantize
-__device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 f = reinterpret_cast<const float4*>(p)[i];
-    v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+// Sixteen consecutive values, as loaded; top() is a bound on their magnitudes as
+// integers in which a NaN or infinity is above every finite value.
+template <typename T>
+struct Raw16;
+template <>
+struct Raw16<__nv_bfloat16> {
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
   }
-}
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[16]) {
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 u = reinterpret_cast<const uint4*>(p)[i];
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (int i = 0; i < 8; ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ uint32_t top(uint32_t t) const {   // two 16-bit maxima
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[8 * i + 2 * k] = bf16_lo(w[k]);
-      v[8 * i + 2 * k + 1] = bf16_hi(w[k]);
+    for (int i = 0; i < 8; ++i) t = __vmaxu2(t, w[i] & 0x7FFF7FFFu);
+    return t;
+  }
+  static __device__ __forceinline__ uint32_t bits(uint32_t t) { return max(t << 16, t & 0xFFFF0000u); }
+  __device__ __forceinline__ void to_f32(float (&v)[16]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[2 * i] = bf16_lo(w[i]);
+      v[2 * i + 1] = bf16_hi(w[i]);
     }
   }
+};
+template <>
+struct Raw16<float> {
+  float v[16];
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 f = reinterpret_cast<const float4*>(p)[i];
+      v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+  }
+  __device__ __forceinline__ uint32_t top(uint32_t t) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t = max(t, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    return t;
+  }
+  static __device__ __forceinline__ uint32_t bits(uint32_t t) { return t; }
+  __device__ __forceinline__ void to_f32(float (&o)[16]) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = v[i];
+  }
+};
+
+__device__ __forceinline__ void mul_pair(float& a, float& b, float s) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "+f"(a), "+f"(b)
+      : "f"(s));
+}
+__device__ __forceinline__ void add_pair(float& a, float& b, float s) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "+f"(a), "+f"(b)
+      : "f"(s));
 }
 
 // Codes of 16 values.  q = x (1/s) is within 2.3e-5 of fl32(x / s) (three
@@ -74,16 +121,23 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[16]) {
 // is that close to halfway; those few values (and rows whose 1/s leaves the
 // normal range) take the division.  Adding 1.5 2^23 rounds to the nearest even
 // integer and leaves it in the low mantissa bits.
-__device__ __forceinline__ uint4 codes16(const float (&v)[16], float s, float inv, bool divide) {
+template <typename T>
+__device__ __forceinline__ uint4 codes16(const Raw16<T>& raw, float s, float inv, bool divide) {
   constexpr float kMagic = 12582912.0f;
-  float r[16], far = 0.0f;
+  float v[16], r[16], far = 0.0f;
+  raw.to_f32(v);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float q = __fmul_rn(v[i], inv);
-    r[i] = __fadd_rn(q, kMagic);
-    far = fmaxf(far, fabsf(__fsub_rn(q, __fsub_rn(r[i], kMagic))));
+  for (int i = 0; i < 16; i += 2) {
+    mul_pair(v[i], v[i + 1], inv);
+    r[i] = v[i];
+    r[i + 1] = v[i + 1];
+    add_pair(r[i], r[i + 1], kMagic);
+    float a = r[i], b = r[i + 1];
+    add_pair(a, b, -kMagic);
+    far = fmaxf(far, fmaxf(fabsf(__fsub_rn(v[i], a)), fabsf(__fsub_rn(v[i + 1], b))));
   }
   if (divide || far > 0.4999f) {
+    raw.to_f32(v);
 #pragma unroll
     for (int i = 0; i < 16; ++i) r[i] = __fadd_rn(fminf(fmaxf(__fdiv_rn(v[i], s), -127.0f), 127.0f), kMagic);
   }
@@ -97,41 +151,44 @@ __device__ __forceinline__ uint4 codes16(const float (&v)[16], float s, float in
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// One row per block.  VPT groups of 16 values per thread stay in registers
-// between the maximum and the codes; wider rows are read a second time.
-template <typename T, int VPT>
-__global__ void __launch_bounds__(1024) int8_quant_kernel(const T* __restrict__ x, int64_t K, int8_t* __restrict__ codes,
-                                                          float* __restrict__ scales) {
-  __shared__ uint32_t red[32];
+// One row per block (or, WARP, one per warp).  VPT groups of 16 values per thread
+// stay in registers between the maximum and the codes; what a wider row has
+// beyond them is read a second time.
+template <typename T, int VPT, bool WARP>
+__global__ void __launch_bounds__(512, 2) int8_quant_kernel(const T* __restrict__ x, int64_t rows, int64_t K,
+                                                         int8_t* __restrict__ codes, float* __restrict__ scales) {
+  __shared__ uint32_t red[16];
   pdl_wait();
   pdl_trigger();
-  const int64_t m = blockIdx.x;
+  const int t = WARP ? (threadIdx.x & 31) : threadIdx.x, nt = WARP ? 32 : blockDim.x;
+  const int64_t m = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+  if (m >= rows) return;          // WARP only: a whole warp
   const T* row = x + m * K;
-  const int groups = (int)(K / 16), t = threadIdx.x, nt = blockDim.x;
-  float v[VPT][16];
-  uint32_t top = 0;   // largest |x| as bits: a NaN or infinity is above every finite value
+  const int groups = (int)(K / 16);
+  Raw16<T> v[VPT];
+  uint32_t top = 0;
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     const int g = t + k * nt;
-    if (g < groups) {
-      load16(row + (int64_t)g * 16, v[k]);
-    } else {
+    if (g < groups)
+      v[k].load(row + (int64_t)g * 16);
+    else
+      v[k].zero();
+  }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[k][i] = 0.0f;
+  for (int k = 0; k < VPT; ++k) top = v[k].top(top);
+  if (!WARP)
+    for (int g = t + VPT * nt; g < groups; g += nt) {
+      Raw16<T> w;
+      w.load(row + (int64_t)g * 16);
+      top = w.top(top);
     }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[k][i]) & 0x7FFFFFFFu);
+  top = __reduce_max_sync(0xffffffffu, Raw16<T>::bits(top));
+  if (!WARP) {
+    if ((t & 31) == 0) red[t >> 5] = top;
+    __syncthreads();
+    top = __reduce_max_sync(0xffffffffu, (t & 31) < (nt >> 5) ? red[t & 31] : 0u);
   }
-  for (int g = t + VPT * nt; g < groups; g += nt) {
-    float w[16];
-    load16(row + (int64_t)g * 16, w);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(w[i]) & 0x7FFFFFFFu);
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
-  if ((t & 31) == 0) red[t >> 5] = top;
-  __syncthreads();
-  top = __reduce_max_sync(0xffffffffu, (t & 31) < (nt >> 5) ? red[t & 31] : 0u);
   const bool finite = top < 0x7F800000u;
   const float s = finite ? __fdiv_rn(__uint_as_float(top), 127.0f) : __uint_as_float(0x7FC00000u);
   if (t == 0) {
@@ -146,28 +203,37 @@ __global__ void __launch_bounds__(1024) int8_quant_kernel(const T* __restrict__ 
     const int g = t + k * nt;
     if (g < groups) out[g] = zero ? make_uint4(0, 0, 0, 0) : codes16(v[k], s, inv, divide);
   }
-  for (int g = t + VPT * nt; g < groups; g += nt) {
-    float w[16];
-    load16(row + (int64_t)g * 16, w);
-    out[g] = zero ? make_uint4(0, 0, 0, 0) : codes16(w, s, inv, divide);
-  }
+  if (!WARP)
+    for (int g = t + VPT * nt; g < groups; g += nt) {
+      Raw16<T> w;
+      w.load(row + (int64_t)g * 16);
+      out[g] = zero ? make_uint4(0, 0, 0, 0) : codes16(w, s, inv, divide);
+    }
+}
+
+template <typename T, int VPT, bool WARP>
+ql_status start_quant(const void* x, int64_t rows, int64_t K, int8_t* codes, float* scales, unsigned threads,
+                      cudaStream_t st) {
+  const int64_t blocks = WARP ? (rows + 7) / 8 : rows;
+  TraceScope ts(TK_INT8, st);
+  QL_CUDA_TRY(launch(int8_quant_kernel<T, VPT, WARP>, dim3((unsigned)blocks), dim3(threads), 0, st, 1, 1, (const T*)x,
+                     rows, K, codes, scales));
+  QL_LAUNCH_CHECK();
+  return QL_OK;
 }
 
 template <typename T>
 ql_status run_quant(const void* x, int64_t rows, int64_t K, int8_t* codes, float* scales, cudaStream_t st) {
+  // 32 registers of a row per thread: with 64 the block has to share an SM with
+  // one other, and spills (28672 x 8192: bf16 130 us, two groups 156; fp32 168 us, four groups 232)
+  constexpr int VPT = sizeof(T) == 2 ? 4 : 2;
   const int64_t groups = K / 16;
-  // one group per thread up to 1024 threads' worth, then two per thread
-  const unsigned threads = (unsigned)std::min<int64_t>((groups + 31) / 32 * 32, 512);
-  const bool two = groups > 512;
-  TraceScope ts(TK_INT8, st);
-  if (two)
-    QL_CUDA_TRY(launch(int8_quant_kernel<T, 2>, dim3((unsigned)rows), dim3(threads), 0, st, 1, 1, (const T*)x, K, codes,
-                       scales));
-  else
-    QL_CUDA_TRY(launch(int8_quant_kernel<T, 1>, dim3((unsigned)rows), dim3(threads), 0, st, 1, 1, (const T*)x, K, codes,
-                       scales));
-  QL_LAUNCH_CHECK();
-  return QL_OK;
+  const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
+  if (groups <= 64) return start_quant<T, 2, true>(x, rows, K, codes, scales, 256, st);     // a row per warp
+  // few rows: as many threads as a row has groups, the shortest way through it
+  const int64_t per = rows <= sms ? 1 : VPT;
+  const unsigned threads = (unsigned)std::min<int64_t>((groups + 32 * per - 1) / (32 * per) * 32, 512);
+  return start_quant<T, VPT, false>(x, rows, K, codes, scales, threads, st);
 }
 
 // ------------------------------------------------------------------- product
