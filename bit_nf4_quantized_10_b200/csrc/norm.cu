@@ -613,13 +613,13 @@ __global__ void __launch_bounds__(kStreamThreads) norm_fwd_stream_kernel(const F
 // memory while a block works and leave it as one part per block; a second
 // kernel adds the parts in a fixed order (no atomics: the same inputs always
 // give the same gradients).
-struct BwdPlan {
-  int blocks;          // blocks of the main kernel
-  int64_t groups;      // gates (1 without)
-  int64_t group_rows;  // rows of one gate
-  int64_t per_group;   // chunks of one gate's rows
-  int64_t chunk_rows;
-  int64_t chunks;
+struct BwdPlan {         // M is below 2^31, so 32 unsigned bits hold any sum of two of these
+  uint32_t blocks;       // blocks of the main kernel
+  uint32_t groups;       // gates (1 without)
+  uint32_t group_rows;   // rows of one gate
+  uint32_t per_group;    // chunks of one gate's rows
+  uint32_t chunk_rows;
+  uint32_t chunks;
 };
 
 struct BwdArgs {
@@ -639,7 +639,7 @@ struct BwdArgs {
   float* part_pre;      // [blocks][D], or NULL
   float* part_post;     // [blocks][D], or NULL
   float* part_s;        // [chunks][D], or NULL
-  int64_t M;
+  uint32_t M;
   int D;
   float alpha, offset, inv_d;
   bool w_f32, post, load_h;
@@ -699,14 +699,14 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const BwdArgs a) 
   // Up to two groups stay in registers between the sums and the results; of more
   // (D > 8192) each is read again, from L2 (four kept spilled: 1000 x 16384 took 257 us).
   constexpr int KEPT = VPT <= 2 ? VPT : 1;
-  for (int64_t chunk = blockIdx.x; chunk < a.plan.chunks; chunk += gridDim.x) {
-    const int64_t grp = chunk / a.plan.per_group;
-    const int64_t group_end = min(a.M, (grp + 1) * a.plan.group_rows);
-    const int64_t row0 = grp * a.plan.group_rows + (chunk % a.plan.per_group) * a.plan.chunk_rows;
-    const int64_t row1 = min(group_end, row0 + a.plan.chunk_rows);
-    const int64_t grow = grp * D;
-    for (int64_t m = row0; m < row1; ++m) {
-      const int64_t flat = m * D;
+  for (uint32_t chunk = blockIdx.x; chunk < a.plan.chunks; chunk += gridDim.x) {
+    const uint32_t grp = chunk / a.plan.per_group;
+    const uint32_t group_end = min(a.M, (grp + 1) * a.plan.group_rows);
+    const uint32_t row0 = grp * a.plan.group_rows + (chunk % a.plan.per_group) * a.plan.chunk_rows;
+    const uint32_t row1 = min(group_end, row0 + a.plan.chunk_rows);
+    const int64_t grow = (int64_t)grp * D;
+    for (uint32_t m = row0; m < row1; ++m) {
+      const int64_t flat = (int64_t)m * D;
       const int shift = GROUPED ? 0 : (int)(flat & 7);
       float n[KEPT][8], u[KEPT][8], nh[KEPT][8], gw[KEPT][8];
       const float rsx = a.dy ? a.rstd_pre[m] : 0.0f;
@@ -810,7 +810,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const BwdArgs a) 
           acc_post[i] += g * sv;
         }
         if (a.part_s) {
-          a.part_s[chunk * D + c] = sv;
+          a.part_s[(int64_t)chunk * D + c] = sv;
         } else if (a.dgate) {
           const float w = !a.w_post ? 1.0f
                           : a.offset + (a.w_f32 ? reinterpret_cast<const float*>(a.w_post)[c]
@@ -881,7 +881,7 @@ __global__ void __launch_bounds__(kBwdStreamThreads) norm_bwd_stream_kernel(cons
 
   // Rows of the block's chunks, one after the other.
   struct Rows {
-    int64_t chunk, row, end, grp;
+    uint32_t chunk, row, end, grp;
   };
   auto open = [&](Rows& r) {     // from r.chunk on, the first chunk with rows
     for (; r.chunk < a.plan.chunks; r.chunk += gridDim.x) {
@@ -893,7 +893,7 @@ __global__ void __launch_bounds__(kBwdStreamThreads) norm_bwd_stream_kernel(cons
   };
   auto issue = [&](const Rows& r, int s) {
     uint8_t* st = ring + (size_t)s * stage_bytes;
-    const int64_t flat = r.row * D;
+    const int64_t flat = (int64_t)r.row * D;
     mbar_arrive_expect_tx(&full_bar[s], (uint32_t)stage_bytes);
     if (a.dy) {
       bulk_load(st + x_off, reinterpret_cast<const XT*>(a.x) + flat, D * (uint32_t)sizeof(XT), &full_bar[s]);
@@ -927,10 +927,10 @@ __global__ void __launch_bounds__(kBwdStreamThreads) norm_bwd_stream_kernel(cons
   const bool sum_s = SUMS && (a.part_post || a.part_s || a.dgate);
   bool first = true;             // no chunk of this block has added to part_post
   int s = 0, use = 0, parity = 0;
-  for (int64_t chunk = blockIdx.x; chunk < a.plan.chunks; chunk += gridDim.x) {
-    const int64_t grp = chunk / a.plan.per_group;
-    const int64_t row0 = grp * a.plan.group_rows + (chunk % a.plan.per_group) * a.plan.chunk_rows;
-    const int64_t row1 = min(min(a.M, (grp + 1) * a.plan.group_rows), row0 + a.plan.chunk_rows);
+  for (uint32_t chunk = blockIdx.x; chunk < a.plan.chunks; chunk += gridDim.x) {
+    const uint32_t grp = chunk / a.plan.per_group;
+    const uint32_t row0 = grp * a.plan.group_rows + (chunk % a.plan.per_group) * a.plan.chunk_rows;
+    const uint32_t row1 = min(min(a.M, (grp + 1) * a.plan.group_rows), row0 + a.plan.chunk_rows);
     if (a.dh) {
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
@@ -938,22 +938,22 @@ __global__ void __launch_bounds__(kBwdStreamThreads) norm_bwd_stream_kernel(cons
         if (c >= D) continue;
         float w[8];
         loadw8<true>(a.w_post, a.w_f32, 0, D, c, D, a.w_post ? a.offset : 1.0f, w);
-        loadw8<true>(a.gate, a.w_f32, grp * D, a.gate_len, c, D, a.gate ? 0.0f : 1.0f, gw[k]);
+        loadw8<true>(a.gate, a.w_f32, (int64_t)grp * D, a.gate_len, c, D, a.gate ? 0.0f : 1.0f, gw[k]);
         mul8(gw[k], w);
       }
     }
     // the rows' factors are asked for one step ahead
     float rsx_next[R], rsh_next[R];
-    auto factors = [&](int64_t m) {
+    auto factors = [&](uint32_t m) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int64_t row = min(m + r, row1 - 1);
+        const uint32_t row = min(m + r, row1 - 1);
         rsx_next[r] = a.dy ? a.rstd_pre[row] : 0.0f;
         rsh_next[r] = a.post ? a.rstd_post[row] : 1.0f;
       }
     };
     if (row0 < row1) factors(row0);
-    for (int64_t m = row0; m < row1; m += R) {
+    for (uint32_t m = row0; m < row1; m += R) {
       float rsx[R], rsh[R], n[R][VPT][8], u[R][VPT][8], sum[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
       Raw8<HT> hraw[R][VPT];         // h as loaded: 4 registers of bf16 where nh takes 8
 #pragma unroll
@@ -962,7 +962,7 @@ __global__ void __launch_bounds__(kBwdStreamThreads) norm_bwd_stream_kernel(cons
         rsh[r] = rsh_next[r];
       }
       if (m + R < row1) factors(m + R);
-      const int rows = (int)min((int64_t)R, row1 - m);
+      const int rows = (int)min((uint32_t)R, row1 - m);
       const int s_first = s;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -1051,7 +1051,7 @@ __global__ void __launch_bounds__(kBwdStreamThreads) norm_bwd_stream_kernel(cons
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (r >= rows) break;
-        const int64_t flat = (m + r) * D;
+        const int64_t flat = (int64_t)(m + r) * D;
         const float k1 = rsx[r] * (sum[3 * r] * a.inv_d);
         const float c2 = (sum[3 * r + 1] - k1 * sum[3 * r + 2]) * a.inv_d;
 #pragma unroll
@@ -1092,7 +1092,7 @@ __global__ void __launch_bounds__(kBwdStreamThreads) norm_bwd_stream_kernel(cons
         float w[8];
         if (a.part_post) {
           float* dst = a.part_post + (int64_t)blockIdx.x * D + c;
-          loadw8<true>(a.gate, a.w_f32, grp * D, a.gate_len, c, D, 0.0f, w);
+          loadw8<true>(a.gate, a.w_f32, (int64_t)grp * D, a.gate_len, c, D, 0.0f, w);
           float old[8];
           if (first) {
 #pragma unroll
@@ -1104,11 +1104,11 @@ __global__ void __launch_bounds__(kBwdStreamThreads) norm_bwd_stream_kernel(cons
           store8_full(dst, old);
         }
         if (a.part_s) {
-          store8_full(a.part_s + chunk * D + c, acc_s[k]);
+          store8_full(a.part_s + (int64_t)chunk * D + c, acc_s[k]);
         } else if (a.dgate) {
           loadw8<true>(a.w_post, a.w_f32, 0, D, c, D, a.w_post ? a.offset : 1.0f, w);
           mul8(w, acc_s[k]);
-          store8_full(a.dgate + grp * D + c, w);
+          store8_full(a.dgate + (int64_t)grp * D + c, w);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc_s[k][j] = 0.0f;
@@ -1167,7 +1167,7 @@ __global__ void __launch_bounds__(kRaggedThreads) norm_bwd_ragged_kernel(const B
   pdl_trigger();
 
   struct Rows {
-    int64_t chunk, row, begin, end, grp;
+    uint32_t chunk, row, begin, end, grp;
   };
   auto open = [&](Rows& r) {     // from r.chunk on, the first chunk with rows
     for (; r.chunk < a.plan.chunks; r.chunk += gridDim.x) {
@@ -1179,7 +1179,7 @@ __global__ void __launch_bounds__(kRaggedThreads) norm_bwd_ragged_kernel(const B
   };
   auto after = [](const Rows& r) {   // the chunk's row after r.row, or its end
     if (r.row + 8 < r.end) return r.row + 8;
-    const int64_t next = (r.row - r.begin) % 8 + 1;
+    const uint32_t next = (r.row - r.begin) % 8 + 1;
     return next < 8 && r.begin + next < r.end ? r.begin + next : r.end;
   };
   auto step = [&](Rows& r) {
@@ -1189,10 +1189,10 @@ __global__ void __launch_bounds__(kRaggedThreads) norm_bwd_ragged_kernel(const B
       open(r);
     }
   };
-  const int64_t total = a.M * D;
+  const int64_t total = (int64_t)a.M * D;
   auto issue = [&](const Rows& r, int s) {
     uint8_t* st = ring + (size_t)s * stage_bytes;
-    const int64_t g0 = r.row * D / 8, g1 = min((r.row * D + D + 7) / 8, total / 8);
+    const int64_t g0 = (int64_t)r.row * D / 8, g1 = min(((int64_t)r.row * D + D + 7) / 8, total / 8);
     const uint32_t n = (uint32_t)(g1 - g0) * 8;
     mbar_arrive_expect_tx(&full_bar[s], n * (uint32_t)((a.dy ? sizeof(XT) + sizeof(YT) : 0) +
                                                        (a.dx_out ? sizeof(XT) : 0) + (a.load_h ? sizeof(HT) : 0)));
@@ -1220,10 +1220,10 @@ __global__ void __launch_bounds__(kRaggedThreads) norm_bwd_ragged_kernel(const B
 #pragma unroll
     for (int j = 0; j < 8; ++j) gw[k][j] = wp[k][j] = 0.0f;
   int s = 0, use = 0, parity = 0, held_shift = -1;
-  int64_t held = -1;
+  uint32_t held = ~0u;
   bool first = true;             // no chunk of this block has added to part_post
   float rsx = 0.0f, rsh = 1.0f, rsx_next = 0.0f, rsh_next = 1.0f;
-  auto factors = [&](int64_t m) {
+  auto factors = [&](uint32_t m) {
     if (a.dy) rsx_next = a.rstd_pre[m];
     if (a.post) rsh_next = a.rstd_post[m];
   };
@@ -1242,7 +1242,8 @@ __global__ void __launch_bounds__(kRaggedThreads) norm_bwd_ragged_kernel(const B
     }
   };
   while (now.chunk < a.plan.chunks) {
-    const int64_t m = now.row, flat = m * D;
+    const uint32_t m = now.row;
+    const int64_t flat = (int64_t)m * D;
     const int shift = (int)(flat & 7);
     const uint8_t* st = ring + (size_t)s * stage_bytes;
     if (now.grp != held || shift != held_shift) {
@@ -1255,7 +1256,7 @@ __global__ void __launch_bounds__(kRaggedThreads) norm_bwd_ragged_kernel(const B
         if (a.dh) {
           float w[8];
           loadw8<false>(a.w_post, a.w_f32, 0, D, c, D, a.w_post ? a.offset : 1.0f, w);
-          loadw8<false>(a.gate, a.w_f32, now.grp * D, a.gate_len, c, D, a.gate ? 0.0f : 1.0f, gw[k]);
+          loadw8<false>(a.gate, a.w_f32, (int64_t)now.grp * D, a.gate_len, c, D, a.gate ? 0.0f : 1.0f, gw[k]);
           mul8(gw[k], w);
         }
         if (a.dy) loadw8<false>(a.w_pre, a.w_f32, 0, D, c, D, a.offset, wp[k]);
@@ -1354,13 +1355,13 @@ __global__ void __launch_bounds__(kRaggedThreads) norm_bwd_ragged_kernel(const B
         acc_s[i] = 0.0f;
         if (a.part_post) {
           float* dst = a.part_post + (int64_t)blockIdx.x * D + c;
-          const float g = value_at(a.gate, a.w_f32, now.grp * D + c);
+          const float g = value_at(a.gate, a.w_f32, (int64_t)now.grp * D + c);
           *dst = first ? g * sv : *dst + g * sv;
         }
         if (a.part_s)
-          a.part_s[now.chunk * D + c] = sv;
+          a.part_s[(int64_t)now.chunk * D + c] = sv;
         else if (a.dgate)
-          a.dgate[now.grp * D + c] = sv * (a.w_post ? a.offset + value_at(a.w_post, a.w_f32, c) : 1.0f);
+          a.dgate[(int64_t)now.grp * D + c] = sv * (a.w_post ? a.offset + value_at(a.w_post, a.w_f32, c) : 1.0f);
       }
       first = false;
       __syncthreads();
@@ -1370,10 +1371,10 @@ __global__ void __launch_bounds__(kRaggedThreads) norm_bwd_ragged_kernel(const B
   __syncthreads();
   // chunks without rows (behind a gate's last, shorter chunk) have no part but zero
   if (a.part_s)
-    for (int64_t chunk = blockIdx.x; chunk < a.plan.chunks; chunk += gridDim.x) {
-      const int64_t grp = chunk / a.plan.per_group, begin = grp * a.plan.group_rows + (chunk % a.plan.per_group) * a.plan.chunk_rows;
+    for (uint32_t chunk = blockIdx.x; chunk < a.plan.chunks; chunk += gridDim.x) {
+      const uint32_t grp = chunk / a.plan.per_group, begin = grp * a.plan.group_rows + (chunk % a.plan.per_group) * a.plan.chunk_rows;
       if (begin < min(a.M, (grp + 1) * a.plan.group_rows)) continue;
-      for (int c = t; c < D; c += nt) a.part_s[chunk * D + c] = 0.0f;
+      for (int c = t; c < D; c += nt) a.part_s[(int64_t)chunk * D + c] = 0.0f;
     }
   for (int c = t; c < D; c += nt) {
     const int i = sum_at<false>(c, D);
@@ -1396,8 +1397,7 @@ struct FinishArgs {
   float* dgate;
   const void* w_post;
   const void* gate;
-  int blocks;
-  int64_t groups, per_group;
+  uint32_t blocks, groups, per_group;
   int D;
   float offset;
   bool w_f32;
@@ -1433,7 +1433,7 @@ __global__ void __launch_bounds__(1024) norm_finish_kernel(const FinishArgs a) {
     const float s = sum_parts(a.part_pre, a.blocks, c, a.D, buf);
     if (writes) a.dw_pre[c] = s;
   } else if (blockIdx.y >= 2) {
-    const int64_t g = blockIdx.y - 2;
+    const int64_t g = (int64_t)blockIdx.y - 2;
     const float s = sum_parts(a.part_s + g * a.per_group * a.D, a.per_group, c, a.D, buf);
     if (writes) a.dgate[g * a.D + c] = s * (a.w_post ? a.offset + value_at(a.w_post, a.w_f32, c) : 1.0f);
   } else if (a.part_post) {
@@ -1472,8 +1472,8 @@ bool bwd_streams(int64_t M, int64_t D) {
 
 BwdPlan bwd_plan(int64_t M, int64_t D, int64_t gate_rows) {
   BwdPlan p;
-  p.group_rows = gate_rows > 0 && gate_rows < M ? gate_rows : M;
-  p.groups = (M + p.group_rows - 1) / p.group_rows;
+  p.group_rows = (uint32_t)(gate_rows > 0 && gate_rows < M ? gate_rows : M);
+  p.groups = (uint32_t)((M + p.group_rows - 1) / p.group_rows);
   const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
   // blocks that an SM holds: of norm_bwd_stream_kernel at 128 registers, or of norm_bwd_kernel
   const int per_sm = bwd_streams(M, D) ? std::max(1, bwd_stream_threads(D) / (int)row_threads(D, bwd_stream_vpt(D)))
@@ -1483,17 +1483,17 @@ BwdPlan bwd_plan(int64_t M, int64_t D, int64_t gate_rows) {
   // through, a gate's chunk end counted as one row, over 1 to 8 chunks a block.
   int64_t best = -1;
   for (int waves = 1; waves <= 8; ++waves) {
-    const int64_t per = std::max<int64_t>(1, std::min(p.group_rows, waves * want / p.groups));
+    const int64_t per = std::max<int64_t>(1, std::min<int64_t>(p.group_rows, waves * want / p.groups));
     const int64_t rows = (p.group_rows + per - 1) / per;
-    const int64_t cost = (p.groups * per + want - 1) / want * (rows + (gate_rows > 0 ? 1 : 0));
+    const int64_t cost = ((int64_t)p.groups * per + want - 1) / want * (rows + (gate_rows > 0 ? 1 : 0));
     if (best < 0 || cost < best) {
       best = cost;
-      p.per_group = per;
-      p.chunk_rows = rows;
+      p.per_group = (uint32_t)per;
+      p.chunk_rows = (uint32_t)rows;
     }
   }
   p.chunks = p.groups * p.per_group;
-  p.blocks = (int)std::min<int64_t>(want, p.chunks);
+  p.blocks = (uint32_t)std::min<int64_t>(want, p.chunks);
   return p;
 }
 
@@ -1720,9 +1720,9 @@ ql_status launch_block_norm_bwd(const ql_block_norm* n, const void* x_out, ql_dt
   a.w_pre = n->w_pre;
   a.w_post = n->w_post;
   a.gate = n->gate;
-  a.gate_len = n->gate ? a.plan.groups * D : 0;
+  a.gate_len = n->gate ? (int64_t)a.plan.groups * D : 0;
   a.dgate = dgate;
-  a.M = M;
+  a.M = (uint32_t)M;
   a.D = (int)D;
   a.alpha = n->alpha;
   a.inv_d = 1.0f / (float)D;
