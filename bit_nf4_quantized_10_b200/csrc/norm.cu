@@ -483,11 +483,13 @@ __global__ void __launch_bounds__(kStreamThreads) norm_fwd_stream_kernel(const F
   pdl_wait();
   pdl_trigger();
   const int64_t total = (int64_t)a.M * D;
+  const uint32_t rows = (uint32_t)a.M;      // below 2^31: a row's number and a few grids more fit
   // The groups that row m touches, as far as they lie inside the tensor: the
   // one group that a last row may share with what is behind the tensor is read
   // from global memory, value by value.
-  auto issue = [&](int64_t m, int s) {
-    const int64_t g0 = m * D / 8, g1 = GROUPED ? (m + 1) * D / 8 : min(((m + 1) * D + 7) / 8, total / 8);
+  auto issue = [&](uint32_t m, int s) {
+    const int64_t flat = (int64_t)m * D;
+    const int64_t g0 = flat / 8, g1 = GROUPED ? (flat + D) / 8 : min((flat + D + 7) / 8, total / 8);
     uint8_t* st = ring + (size_t)s * stage_bytes;
     const uint32_t n = (uint32_t)(g1 - g0) * 8;
     mbar_arrive_expect_tx(&full_bar[s], n * (uint32_t)(sizeof(XT) + (HAS_H ? sizeof(HT) : 0)));
@@ -498,13 +500,13 @@ __global__ void __launch_bounds__(kStreamThreads) norm_fwd_stream_kernel(const F
   };
   if (t == 0)
     for (int s = 0; s < stages; ++s)
-      if (blockIdx.x + (int64_t)s * gridDim.x < a.M) issue(blockIdx.x + (int64_t)s * gridDim.x, s);
+      if (blockIdx.x + s * gridDim.x < rows) issue(blockIdx.x + s * gridDim.x, s);
 
   float gw[VPT][8];
   int held = -1, held_shift = 0;   // the gate row in gw, and where its groups start
   int s = 0, use = 0, parity = 0;
-  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
-    const int64_t flat = m * D;
+  for (uint32_t m = blockIdx.x; m < rows; m += gridDim.x) {
+    const int64_t flat = (int64_t)m * D;
     const int shift = GROUPED ? 0 : (int)(flat & 7);
     const int grow = a.gate ? (int)m / a.gate_rows : 0;
     const bool fresh = grow != held || shift != held_shift;
@@ -575,7 +577,7 @@ __global__ void __launch_bounds__(kStreamThreads) norm_fwd_stream_kernel(const F
     float sum[1] = {s0 + s1};
     block_sums(sum, red[parity]);   // also: every thread has read the stage
     parity ^= 1;
-    if (t == 0 && m + (int64_t)stages * gridDim.x < a.M) issue(m + (int64_t)stages * gridDim.x, s);
+    if (t == 0 && m + stages * gridDim.x < rows) issue(m + stages * gridDim.x, s);
     if (++s == stages) {
       s = 0;
       ++use;
