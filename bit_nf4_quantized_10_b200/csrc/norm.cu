@@ -14,11 +14,11 @@
 // (backward) fp32 operations per element, so both directions are bound by HBM.
 // Measured on bf16 streams (events, inputs beyond L2; a plain copy moves 6.45 TB/s):
 //   forward   8192 x 8192, a gate per sequence        92 us  5.8 TB/s
-//             1001 x 2051, fp32 stream              11.6 us  (the rows' latency)
+//             1001 x 2051, fp32 stream              11.6 us  (instructions: odd widths)
 //             4 x 8192                               3.6 us  (the launch)
-//   backward  8192 x 4096, dy fp32, frozen norms      80 us  5.9 TB/s
-//             the same with all weight gradients      94 us  5.0 TB/s
-//             8000 x 2051, all weight gradients      122 us  1.9 TB/s
+//   backward  8192 x 4096, dy fp32, frozen norms      73 us  6.4 TB/s
+//             the same with all weight gradients      90 us  5.2 TB/s
+//             8000 x 2051, all weight gradients      112 us  2.1 TB/s
 //             64 x 4096, frozen norms                3.3 us  (the launch)
 //
 // Layout: the elements of all [M, D] tensors are taken in groups of 8 at flat
@@ -840,8 +840,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const BwdArgs a) 
 // barrier, after which its stage is free: by then the row is in registers.
 //   D <= 4096: one group a thread, R = 2 rows at a time, which share the barrier;
 //   gate (o + w_post), o + w_pre and the column sums stay in registers (8192 x
-//   4096 with all gradients: 94 us; a row at a time 100, two groups a thread
-//   in two blocks an SM 106 to 110, the kernel above 140).
+//   4096 with all gradients: 90 us; a row at a time, with 64-bit rows, 100 against
+//   94; two groups a thread in two blocks an SM 106 to 110; the kernel above 140).
 //   D <= 8192: two groups, one row; 128 registers do not hold all of that, so the
 //   sum for dw_pre is in shared memory and w_pre is read again for every row.
 constexpr int kBwdStreamThreads = 512;
@@ -1138,8 +1138,9 @@ __global__ void __launch_bounds__(kBwdStreamThreads) norm_bwd_stream_kernel(cons
 // from the second, ...), so that the weights in registers serve several rows.
 // The column sums are in shared memory, where any thread adds to any column, a
 // barrier between rows.  Instructions bound it (shifted weights, edge groups and
-// the sums value by value): 8000 x 2051 122 us, norm_bwd_kernel 171; 4096 x 4097
-// 122 against 149, 16000 x 1001 127 against 165, 4000 x 8001 269 against 289.
+// the sums value by value): 8000 x 2051 112 us, norm_bwd_kernel 171; 4000 x 8001
+// 217 against 289; with 64-bit rows 4096 x 4097 122 against 149, 16000 x 1001 127
+// against 165.
 constexpr int kRaggedThreads = 576;   // 112 registers: one block of a row of 4600 values, two of 2300
 
 template <typename XT, typename HT, typename YT, int VPT>
@@ -1543,7 +1544,9 @@ template <typename XT, typename HT, bool GROUPED>
 ql_status pick_fwd(const FwdArgs& a, cudaStream_t st) {
   const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
   const int groups = row_groups(a.D);
-  if (groups > 128 && groups <= kStreamVpt * kStreamThreads && a.M > sms)
+  // more rows than SMs are streamed, even narrow ones (8192 x 512: 10.6 us, a row
+  // per warp 15.6; 8192 x 999: 32 against 62)
+  if (groups >= 8 && groups <= kStreamVpt * kStreamThreads && a.M > sms)
     return a.h ? a.w_f32 ? run_stream<XT, HT, float, GROUPED, true>(a, st) : run_stream<XT, HT, bf16, GROUPED, true>(a, st)
            : a.w_f32 ? run_stream<XT, XT, float, GROUPED, false>(a, st) : run_stream<XT, XT, bf16, GROUPED, false>(a, st);
   // rows of up to 128 groups: one warp each, no block barrier
