@@ -291,6 +291,12 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map,
       : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap* map, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
 // Arrive on this CTA's barrier alone once every pair MMA issued so far has completed.
 __device__ __forceinline__ void mma_commit_pair_local(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -396,16 +402,22 @@ __global__ void __launch_bounds__(THREADS, 1)
   cluster_sync();   // both CTAs' barriers are initialised and TMEM is allocated
   tc_fence_after();
   const uint32_t tmem = *tmem_addr;
+  Work w;
+  // While the kernel in front (the tokens' quantization, as a rule) finishes, the
+  // first stages of the weight come into L2.  Nothing is read yet: what that kernel
+  // still writes is in L2 too.  (8 tokens, 28672 x 8192: 44.0 -> 42.9 us; not for tiles
+  // split along K, whose few stages gained nothing: 1 x 4096 x 4096 12.7 us, 13.7 with it.)
+  if (warp == 0 && p.plan.splits == 1 && work_at(p.plan, pair, 0, w) && elect_one()) {
+    prefetch_tmap(&map_w);
+    prefetch_tmap(&map_x);
+    const int wrow = w.tile / p.plan.token_tiles * BW + rank * (BW / 2);
+    for (int k = w.k0; k < min(w.k1, w.k0 + S); ++k) tma_prefetch(&map_w, k * BK, wrow);
+  }
   pdl_wait();
   pdl_trigger();
 
-  Work w;
   if (warp == 0) {
     {
-      if (elect_one()) {
-        prefetch_tmap(&map_w);
-        prefetch_tmap(&map_x);
-      }
       // one thread issues every copy of a stage, so the loop is kept short: the
       // ring's position is counted, not divided out
       const uint32_t full0 = cluster_map(smem_u32(full), 0);   // the even CTA's barriers

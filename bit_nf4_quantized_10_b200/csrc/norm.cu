@@ -454,9 +454,6 @@ constexpr int kStreamVpt = 2;
 constexpr int kStreamThreads = 1024;
 constexpr int kMaxStages = 4;
 
-template <typename XT, typename HT>
-__host__ __device__ constexpr int stream_x_bytes(int groups) { return groups * 8 * (int)sizeof(XT); }
-
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                    smem_u32(dst)),
@@ -1659,7 +1656,7 @@ int64_t block_norm_max_d() { return bn::kMaxD; }
 // Parts of the column sums, carved in this order (each piece 256-byte aligned):
 //   dw_pre [blocks, D], dw_post [blocks, D], S [chunks, D] (gates of several chunks).
 size_t block_norm_bwd_ws(int64_t M, int64_t D, int64_t gate_rows) {
-  if (M <= 0 || D <= 0 || D > bn::kMaxD || gate_rows < 0) return 0;
+  if (M <= 0 || M >= ((int64_t)1 << 31) || D <= 0 || D > bn::kMaxD || gate_rows < 0) return 0;
   const bn::BwdPlan p = bn::bwd_plan(M, D, gate_rows);
   size_t b = 2 * bn::align256((size_t)p.blocks * D * 4);
   if (gate_rows > 0 && p.per_group > 1) b += bn::align256((size_t)p.chunks * D * 4);

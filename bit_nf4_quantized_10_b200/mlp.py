@@ -100,8 +100,8 @@ class QLoRAMLPStack:
     lists by norm, None where a norm has no such weight)."""
 
     def __init__(self, mlps, norms, stream_dtype=torch.bfloat16, train_norms: bool = False):
-        if len(norms) != len(mlps) + 1:
-            raise ValueError("one norm more than MLPs")
+        if not mlps or len(norms) != len(mlps) + 1:
+            raise ValueError("at least one MLP, and one norm more than MLPs")
         if norms[0].w_pre is None or norms[0].w_post is not None or norms[0].gate is not None or norms[0].alpha != 1.0:
             raise ValueError("the first norm has no block in front of it: w_pre alone, alpha 1")
         if any(n.w_pre is None for n in norms[:-1]):
