@@ -13,7 +13,7 @@
 // Every value is read once and written once; about 15 (forward) and 30
 // (backward) fp32 operations per element, so both directions are bound by HBM.
 // Measured on bf16 streams (events, inputs beyond L2; a plain copy moves 6.45 TB/s):
-//   forward   8192 x 8192, a gate per sequence        92 us  5.8 TB/s
+//   forward   8192 x 8192, a gate per sequence        91 us  5.9 TB/s
 //             1001 x 2051, fp32 stream              11.6 us  (instructions: odd widths)
 //             4 x 8192                               3.6 us  (the launch)
 //   backward  8192 x 4096, dy fp32, frozen norms      73 us  6.4 TB/s
@@ -334,6 +334,11 @@ __device__ __forceinline__ float value_at(const void* p, bool f32, int64_t i) {
   return f32 ? reinterpret_cast<const float*>(p)[i] : to_f32(reinterpret_cast<const bf16*>(p)[i]);
 }
 
+// (mean + eps)^-1/2, the mean rounded before eps is added.
+__device__ __forceinline__ float rstd_of(float sum, float inv_d, float eps) {
+  return rsqrtf(__fadd_rn(__fmul_rn(sum, inv_d), eps));
+}
+
 struct FwdArgs {
   const void* x;
   const void* h;
@@ -394,7 +399,7 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxThreads) norm_fwd_kernel(cons
 #pragma unroll
         for (int j = 0; j < 8; ++j) s[0] += hv[v][j] * hv[v][j];
       if (WARP) warp_sums(s); else block_sums(s, red[0]);
-      rs = rsqrtf(s[0] * a.inv_d + a.eps);
+      rs = rstd_of(s[0], a.inv_d, a.eps);
       if (t == 0 && a.rstd_post) a.rstd_post[m] = rs;
     }
     const int64_t grow = a.gate ? (int64_t)(m / a.gate_rows) * D : 0;
@@ -404,8 +409,10 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxThreads) norm_fwd_kernel(cons
       float wv[8], gv[8];
       loadw8<GROUPED>(a.w_post, a.w_f32, 0, D, col[v], D, a.w_post ? a.offset : 1.0f, wv);
       loadw8<GROUPED>(a.gate, a.w_f32, grow, a.gate_len, col[v], D, a.gate ? 0.0f : 1.0f, gv);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) r[v][j] = a.alpha * r[v][j] + gv[j] * (hv[v][j] * rs * wv[j]);
+      mul8(hv[v], rs);
+      mul8(hv[v], wv);
+      mul8(hv[v], gv);
+      fma8(r[v], a.alpha, r[v], hv[v]);
     }
   } else {
 #pragma unroll
@@ -426,7 +433,7 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxThreads) norm_fwd_kernel(cons
   }
   if (!a.y) return;
   if (WARP) warp_sums(s); else block_sums(s, red[1]);
-  const float rs = rsqrtf(s[0] * a.inv_d + a.eps);
+  const float rs = rstd_of(s[0], a.inv_d, a.eps);
   if (t == 0 && a.rstd_pre) a.rstd_pre[m] = rs;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
@@ -446,10 +453,14 @@ __global__ void __launch_bounds__(WARP ? 256 : kMaxThreads) norm_fwd_kernel(cons
 // gridDim.x, ...; their x and h arrive by bulk copies in a ring of `stages`
 // rows in shared memory, so the next rows are on their way while this one waits
 // for its two sums.  Two groups per thread; 64 registers, so 1024 threads an SM
-// are at work.  The product gate (o + w_post) stays in registers while the gate's
-// row does not change; w_pre comes from L1, asked for ahead of the second sum.
+// are at work.  The gate (or, without one, o + w_post) stays in registers while
+// its row does not change; the other weights come from L1, w_pre asked for ahead
+// of the second sum.  The products are taken in the formula's order, h rstd w gate,
+// each rounded: x' then lies on the same side of a bf16 rounding border as in
+// any other evaluation in that order, but where rstd's last bit differs.
 // 8192 x 8192: 107 us so far; 97 without divisions in the row loop and with
-// paired bf16 rounding; 92 with packed fp32 pairs and w_pre ahead of the barrier.
+// paired bf16 rounding; 92 with packed fp32 pairs and w_pre ahead of the barrier;
+// 90.5 with two rows in the ring instead of three.
 constexpr int kStreamVpt = 2;
 constexpr int kStreamThreads = 1024;
 constexpr int kMaxStages = 4;
@@ -529,16 +540,16 @@ __global__ void __launch_bounds__(kStreamThreads) norm_fwd_stream_kernel(const F
         if (!GROUPED && (c < 0 || c + 8 > D)) mask8(v[k], c, D);
         dot8(s0, s1, v[k], v[k]);
         if (fresh) {
-          float w[8];
-          loadw8<GROUPED>(a.w_post, sizeof(WT) == 4, 0, D, c, D, a.w_post ? a.offset : 1.0f, w);
-          loadw8<GROUPED>(a.gate, sizeof(WT) == 4, (int64_t)grow * D, a.gate_len, c, D, a.gate ? 0.0f : 1.0f, gw[k]);
-          mul8(gw[k], w);
+          if (a.gate)
+            loadw8<GROUPED>(a.gate, sizeof(WT) == 4, (int64_t)grow * D, a.gate_len, c, D, 0.0f, gw[k]);
+          else
+            loadw8<GROUPED>(a.w_post, sizeof(WT) == 4, 0, D, c, D, a.w_post ? a.offset : 1.0f, gw[k]);
         }
       }
       if (a.w_post) {
         float sum[1] = {s0 + s1};
         block_sums(sum, red[2]);
-        rs = rsqrtf(sum[0] * a.inv_d + a.eps);
+        rs = rstd_of(sum[0], a.inv_d, a.eps);
         if (t == 0 && a.rstd_post) a.rstd_post[m] = rs;
       }
       s0 = s1 = 0.0f;
@@ -558,6 +569,11 @@ __global__ void __launch_bounds__(kStreamThreads) norm_fwd_stream_kernel(const F
       }
       if (HAS_H) {
         mul8(v[k], rs);
+        if (a.gate && a.w_post) {
+          float w[8];
+          loadw8<GROUPED>(a.w_post, sizeof(WT) == 4, 0, D, c, D, a.offset, w);
+          mul8(v[k], w);
+        }
         mul8(v[k], gw[k]);
         fma8(v[k], a.alpha, xv, v[k]);
       } else {
@@ -580,7 +596,7 @@ __global__ void __launch_bounds__(kStreamThreads) norm_fwd_stream_kernel(const F
       ++use;
     }
     if (a.y) {
-      const float rx = rsqrtf(sum[0] * a.inv_d + a.eps);
+      const float rx = rstd_of(sum[0], a.inv_d, a.eps);
       if (t == 0 && a.rstd_pre) a.rstd_pre[m] = rx;
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
@@ -1524,10 +1540,12 @@ ql_status run_stream(const FwdArgs& a, cudaStream_t st) {
   const int groups = row_groups(a.D);
   const unsigned threads = row_threads(a.D, kStreamVpt);
   const int stage = groups * 8 * (int)(sizeof(XT) + (HAS_H ? sizeof(HT) : 0));
-  // as many blocks as 1024 threads an SM allow, if two rows each fit; then as many rows as fit
+  // as many blocks as 1024 threads an SM allow, if two rows each fit.  No third row:
+  // the shared memory serves better as L1, which the weights come from (8192 x
+  // 8192: 94.6 -> 90.5 us, 8192 x 4096: 53 -> 49).
   int per_sm = std::max(1, kStreamThreads / (int)threads);
   while (per_sm > 1 && per_sm * (2 * stage + 2048) > kMost) --per_sm;
-  const int stages = std::max(1, std::min(kMaxStages, (kMost / per_sm - 2048) / stage));
+  const int stages = std::max(1, std::min(2, (kMost / per_sm - 2048) / stage));
   const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
   // a multiple of 8 blocks: 8 rows on, a row starts at the same place of a group
   const int64_t grid = std::min<int64_t>(a.M, (int64_t)sms * per_sm / 8 * 8);
