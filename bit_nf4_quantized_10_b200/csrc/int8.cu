@@ -1,6 +1,6 @@
 // 8-bit integer linear: rows quantized to int8 with one scale each, and the
 // product of two such operands on the tensor cores (tcgen05 kind::i8):
-//   s_m = fl32(max_k |x[m, k]| / 127),  a[m, k] = rint(fl32(x[m, k] / s_m))
+//   s_m = fl32(max_k |x[m, k]| fl32(1/127)),  a[m, k] = rint(fl32(x[m, k] / s_m))
 //   Y[m, n] = fl32(acc) * fl32(s_a[m] s_b[n]),  acc = sum_k a[m, k] b[n, k]
 // acc is exact (int32), so it does not depend on how K is split.
 //
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(512, 2) int8_quant_kernel(const T* __restrict_
     top = __reduce_max_sync(0xffffffffu, (t & 31) < (nt >> 5) ? red[t & 31] : 0u);
   }
   const bool finite = top < 0x7F800000u;
-  const float s = finite ? __fdiv_rn(__uint_as_float(top), 127.0f) : __uint_as_float(0x7FC00000u);
+  const float s = finite ? __fmul_rn(__uint_as_float(top), 1.0f / 127.0f) : __uint_as_float(0x7FC00000u);
   if (t == 0) {
     scales[m] = s;
     if (!finite) raise_status(ST_NONFINITE);

@@ -511,7 +511,7 @@ ql_status qlora_block_norm_bwd(const ql_block_norm* norm, const void* x_out, ql_
  * a merged weight (qlora_merge), not the QLoRA linear's bf16 activations.
  *
  * int8_quantize: x device [rows, K] of x_dt -> codes device out int8 [rows, K],
- *   scales device out fp32 [rows]:  s = fl32(max|x| / 127), code =
+ *   scales device out fp32 [rows]:  s = fl32(max|x| fl32(1/127)), code =
  *   rint(fl32(x / s)) (ties to even) in [-127, 127], 0 where s == 0.  A row with
  *   a NaN or infinity sets QL_ERR_NONFINITE in the status word; its codes are 0
  *   and its scale NaN, so that its products are NaN.

@@ -1,7 +1,7 @@
 """Row-wise int8 quantization and the product of two such operands
 (int8_quantize / int8_gemm).
 
-  s = fl32(max|x| / 127), code = rint(fl32(x / s)) (ties to even) clipped to
+  s = fl32(max|x| fl32(1/127)), code = rint(fl32(x / s)) (ties to even) clipped to
   [-127, 127], 0 where s == 0;  Y = (sum_k a b) s_a s_b.
 The scale and the quotient are fp32 values by definition, so the codes are
 whole numbers that an implementation matches exactly.
@@ -14,7 +14,7 @@ import numpy as np
 def quantize(x):
     """x: float32 array [rows, K] -> (int8 codes, float32 scales)."""
     x = np.asarray(x, dtype=np.float32)
-    s = np.max(np.abs(x), axis=1) / np.float32(127.0)
+    s = np.max(np.abs(x), axis=1) * (np.float32(1.0) / np.float32(127.0))
     with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
         q = np.where(s[:, None] > 0, x / s[:, None], np.float32(0.0))
     assert s.dtype == np.float32 and q.dtype == np.float32

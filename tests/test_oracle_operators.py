@@ -61,7 +61,7 @@ def test_int8_codes_against_rationals():
     """Codes are the nearest integers to the fp32 quotient (ties to even), decided here on exact rationals."""
     rng = np.random.default_rng(0)
     x = (rng.standard_normal((6, 64)) * np.array([1, 1e-3, 50, 1e-30, 1e30, 1]).reshape(6, 1)).astype(np.float32)
-    x[5] = np.arange(64) - 31.5           # top 32: s = fl32(32 / 127)
+    x[5] = np.arange(64) - 31.5           # top 32: s = fl32(32 fl32(1/127))
     x[0, 0] = 127.0 * 2.0 ** 3            # s = 8 exactly: multiples of 4 are ties
     x[0, 1:9] = [4, 12, 20, -4, -12, 28, 36, -20]
     codes, s = int8.quantize(x)
