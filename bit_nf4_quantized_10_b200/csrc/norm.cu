@@ -14,7 +14,7 @@
 // (backward) fp32 operations per element, so both directions are bound by HBM.
 // Measured on bf16 streams (events, inputs beyond L2; a plain copy moves 6.45 TB/s):
 //   forward   8192 x 8192, a gate per sequence        91 us  5.9 TB/s
-//             1001 x 2051, fp32 stream              11.6 us  (instructions: odd widths)
+//             1001 x 2051, fp32 stream              12.6 us  (instructions: odd widths)
 //             4 x 8192                               3.6 us  (the launch)
 //   backward  8192 x 4096, dy fp32, frozen norms      73 us  6.4 TB/s
 //             the same with all weight gradients      90 us  5.2 TB/s
