@@ -417,40 +417,38 @@ __global__ void __launch_bounds__(THREADS, 1)
   pdl_trigger();
 
   if (warp == 0) {
-    {
-      // one thread issues every copy of a stage, so the loop is kept short: the
-      // ring's position is counted, not divided out
-      const uint32_t full0 = cluster_map(smem_u32(full), 0);   // the even CTA's barriers
-      int s = 0, use = 0;
-      bool ok = true;
-      for (int i = 0; ok && work_at(p.plan, pair, i, w); ++i) {
-        const int wrow = w.tile / p.plan.token_tiles * BW + rank * (BW / 2);
-        const int xrow = w.tile % p.plan.token_tiles * tn + rank * (tn / 2);
-        for (int k = w.k0; k < w.k1; ++k) {
-          if (use > 0 && !warp_wait(&empty[s], (use - 1) & 1, abort_flag, p.wait_limit)) {
-            ok = false;
-            break;
-          }
-          uint8_t* st = ring + s * p.stage_bytes;
-          if (elect_one()) {
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)p.stage_bytes);
-            tma_load_pair(st, &map_w, full0 + 8u * s, k * BK, wrow);
-            tma_load_pair(st + A_BYTES, &map_x, full0 + 8u * s, k * BK, xrow);
-          }
-          if (++s == S) {
-            s = 0;
-            ++use;
-          }
+    // one thread issues every copy of a stage, so the loop is kept short: the
+    // ring's position is counted, not divided out
+    const uint32_t full0 = cluster_map(smem_u32(full), 0);   // the even CTA's barriers
+    int s = 0, use = 0;
+    bool ok = true;
+    for (int i = 0; ok && work_at(p.plan, pair, i, w); ++i) {
+      const int wrow = w.tile / p.plan.token_tiles * BW + rank * (BW / 2);
+      const int xrow = w.tile % p.plan.token_tiles * tn + rank * (tn / 2);
+      for (int k = w.k0; k < w.k1; ++k) {
+        if (use > 0 && !warp_wait(&empty[s], (use - 1) & 1, abort_flag, p.wait_limit)) {
+          ok = false;
+          break;
         }
-      }
-      // a stage is empty once its copies have landed and the MMAs have read it:
-      // no copy may still be landing, and no commit arriving, when the CTA exits
-      for (int r = 0; r < S; ++r) {
-        if (use > 0) warp_wait(&empty[s], (use - 1) & 1, abort_flag, p.wait_limit);
+        uint8_t* st = ring + s * p.stage_bytes;
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)p.stage_bytes);
+          tma_load_pair(st, &map_w, full0 + 8u * s, k * BK, wrow);
+          tma_load_pair(st + A_BYTES, &map_x, full0 + 8u * s, k * BK, xrow);
+        }
         if (++s == S) {
           s = 0;
           ++use;
         }
+      }
+    }
+    // a stage is empty once its copies have landed and the MMAs have read it:
+    // no copy may still be landing, and no commit arriving, when the CTA exits
+    for (int r = 0; r < S; ++r) {
+      if (use > 0) warp_wait(&empty[s], (use - 1) & 1, abort_flag, p.wait_limit);
+      if (++s == S) {
+        s = 0;
+        ++use;
       }
     }
   } else if (warp == 1) {

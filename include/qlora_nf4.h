@@ -31,7 +31,8 @@
  *     CUDA device and be 16-byte aligned.  The library never allocates or frees
  *     caller memory; the caller owns every buffer, including the workspace.
  *   - `stream` is a cudaStream_t (NULL = legacy default stream).  Every call
- *     is asynchronous on that stream.
+ *     is asynchronous on that stream.  Calls that may run at the same time need
+ *     workspaces of their own.
  *   - Argument errors return QL_ERR_INVALID_ARG / QL_ERR_UNSUPPORTED /
  *     QL_ERR_WORKSPACE synchronously, before anything is launched.  A failed
  *     launch returns QL_ERR_CUDA.  Conditions the device detects (a non-finite
